@@ -20,7 +20,22 @@ __all__ = [
     "qv_status_string", "qv_hadamard_smooth_quant", "qv_pack_weights", "qv_w4a4_gemm",
     "qv_w4a4_linear_workspace_size", "qv_w4a4_linear", "qv_w4a4_linear_noalloc", "qv_smooth_calibrate",
     "QV_NOALLOC_SCRATCH_BYTES", "qv_w4a4_gemm_requant", "qv_w4a4_gemm_requant_workspace_size",
+    # single-token entry points (decode.py)
+    "qv_w4a16_gemv", "qv_w4a16_linear", "qv_w4a16_linear_workspace_size", "QVKVCache", "qv_kv_append",
+    "qv_paged_attention", "qv_paged_attention_workspace_size", "QV_KV_BF16", "QV_KV_INT8",
 ]
+
+_DECODE = frozenset(__all__[__all__.index("qv_w4a16_gemv"):])
+
+
+def __getattr__(name: str):
+    """The single-token entry points come with torch, which this module itself imports only when it is used."""
+    if name in _DECODE:
+        from . import decode
+
+        globals().update({n: getattr(decode, n) for n in _DECODE})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libqv.so")

@@ -1,0 +1,384 @@
+// paged_attention.hip -- attention of one new token of every sequence over a paged cache of keys and
+// values (bf16, or int8 with a scale per token and head).
+//
+//   O[b][i] = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q_i . k_t - m),  m the running maximum
+//
+// One pass over the keys and values, which is all there is to move: the kernel is bound by memory.  The
+// length is split into parts over the grid so that few sequences still fill the chip, and a second
+// kernel joins the parts by their maxima and sums.
+//
+// A wave takes 16 tokens a tile and the up to 16 query heads that share a cache head, and nothing leaves
+// its registers between the two products:
+//   S^T = K q^T   v_mfma_f32_16x16x32_bf16: lane (r = lane % 16, c = lane / 16) loads 16 bytes of token r's
+//                 key as they lie in memory; it gets the scores of tokens 4 c + i (i < 4) for query r.
+//   O^T += V^T P^T  v_mfma_f32_16x16x4f32: step i contracts the four tokens 4 c + i, so lane (r, c)'s score
+//                 number i already is the operand, unrounded, and the other operand is value
+//                 channel D / 16 r + e of token 4 c + i: D / 16 neighbouring channels of one token,
+//                 one load.  The result has query r in lane (r, c), channels 4 D / 16 c onwards, next to
+//                 that query's maximum and sum.
+// The order of channels inside S and of tokens inside O is free, which is what makes both loads contiguous.
+// With one query per cache head 15 of 16 columns repeat it; the matrix cores have the room (at D =
+// 128 and bf16 a tile's 32 + 4 MFMAs take about a third of the time its 8 KB take to arrive).
+#include <hip/hip_bf16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qv_decode_internal.h"
+
+namespace qv {
+
+namespace {
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kTile = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.402823466e38f;  // finite, so that differences of maxima are never inf - inf
+
+struct Args {
+  const void* q;
+  void* o;
+  const char *kp, *vp;
+  const float *ks, *vs;
+  const int32_t *table, *lens;
+  float* partial;  // [B * q_heads][splits][D], then [B * q_heads][splits][2] (maximum, sum)
+  int64_t q_ts, q_hs, o_ts, o_hs, page_stride, head_stride, ld_table, num_pages;
+  int64_t capacity, window;
+  uint32_t B, heads, q_heads, share, q_tiles, splits, token_stride, page_size;
+  float scale;  // times log2 e
+};
+
+__device__ __forceinline__ float bits_float(unsigned u) { return __builtin_bit_cast(float, u); }
+__device__ __forceinline__ unsigned float_bits(float f) { return __builtin_bit_cast(unsigned, f); }
+
+// Tiles [first, last) of a sequence's attended tokens and the tiles of a part of them.
+struct Span {
+  int64_t begin, end;  // tokens
+  int64_t first, last;
+  int64_t per_part;
+};
+__device__ __forceinline__ Span span_of(const Args& a, uint32_t b) {
+  Span s;
+  int64_t n = a.lens[b];
+  n = n < 0 ? 0 : (n > a.capacity ? a.capacity : n);
+  s.end = n;
+  s.begin = a.window > 0 && n > a.window ? n - a.window : 0;
+  s.first = s.begin / kTile;
+  s.last = (n + kTile - 1) / kTile;
+  int64_t per = (s.last - s.first + a.splits - 1) / a.splits;
+  const int64_t least = kMinTokensPerPart / kTile;
+  s.per_part = per < least ? least : per;
+  return s;
+}
+
+// Keys of one tile as loaded, and as operands of the score product.
+template <int D, bool INT8>
+struct Keys {
+  static constexpr int kLoads = INT8 ? D / 64 : D / 32;
+  u32x4 d[kLoads];
+  __device__ __forceinline__ void load(const char* tile, uint32_t token_bytes, int c) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      d[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(tile + token_bytes + 64 * j + 16 * c));
+  }
+  // operand f covers channels channel(f, c) .. + 7
+  static __device__ __forceinline__ int channel(int f, int c) {
+    return INT8 ? 64 * (f >> 1) + 16 * c + 8 * (f & 1) : 32 * f + 8 * c;
+  }
+  __device__ __forceinline__ bf16x8 operand(int f) const {
+    if constexpr (!INT8) {
+      return __builtin_bit_cast(bf16x8, d[f]);
+    } else {
+      u32x4 o;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned w = d[f >> 1][2 * (f & 1) + h];
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));  // exact in bf16
+        o[2 * h] = __builtin_amdgcn_perm(float_bits(x[1]), float_bits(x[0]), 0x07060302u);
+        o[2 * h + 1] = __builtin_amdgcn_perm(float_bits(x[3]), float_bits(x[2]), 0x07060302u);
+      }
+      return __builtin_bit_cast(bf16x8, o);
+    }
+  }
+};
+
+// Channels kE r .. kE r + kE - 1 of one token's value.
+template <int D, bool INT8>
+struct Values {
+  static constexpr int kE = D / 16;
+  static constexpr int kBytes = kE * (INT8 ? 1 : 2);
+  static constexpr int kWords = kBytes / 4;
+  unsigned d[kWords];
+  __device__ __forceinline__ void load(const char* p) {
+    if constexpr (kWords == 4) {
+      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+      d[0] = v[0], d[1] = v[1], d[2] = v[2], d[3] = v[3];
+    } else if constexpr (kWords == 2) {
+      const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+      d[0] = v[0], d[1] = v[1];
+    } else {
+      d[0] = __builtin_nontemporal_load(reinterpret_cast<const unsigned*>(p));
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (INT8) return (float)(int8_t)(d[e >> 2] >> (8 * (e & 3)));
+    return (e & 1) ? bits_float(d[e >> 1] & 0xFFFF0000u) : bits_float(d[e >> 1] << 16);
+  }
+};
+
+__device__ __forceinline__ void store(float* o, float v) { *o = v; }
+__device__ __forceinline__ void store(__hip_bfloat16* o, float v) { *o = __float2bfloat16(v); }
+
+template <int D, typename X, bool INT8>
+__global__ __launch_bounds__(kThreads) void attention_kernel(Args a) {
+  constexpr int NP = sizeof(X) == 2 ? 1 : 3;  // bf16 pieces of a query
+  constexpr int kF = D / 32;                  // operands of the score product
+  constexpr int kE = D / 16;
+  constexpr int kElem = INT8 ? 1 : 2;
+  constexpr int kU = 2;  // tiles at a time
+  __shared__ float red_o[kWaves][kTile][D + 4];
+  __shared__ float red_m[kWaves][kTile], red_l[kWaves][kTile];
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, c = lane >> 4;
+  uint32_t id = blockIdx.x;
+  const uint32_t part = id % a.splits;
+  id /= a.splits;
+  const uint32_t q_tile = id % a.q_tiles;
+  id /= a.q_tiles;
+  const uint32_t h = id % a.heads, b = id / a.heads;
+  const uint32_t q0 = q_tile * kTile;
+  const int queries = (int)(a.share - q0 < kTile ? a.share - q0 : kTile);
+
+  const Span sp = span_of(a, b);
+  const int64_t first = sp.first + part * sp.per_part;
+  const int64_t last = first + sp.per_part < sp.last ? first + sp.per_part : sp.last;
+  if (first >= last && part > 0) return;
+
+  const int mine = r < queries ? r : queries - 1;
+  bf16x8 q[kF][NP];
+  {
+    const X* row = static_cast<const X*>(a.q) + b * a.q_ts + (int64_t)(h * a.share + q0 + mine) * a.q_hs;
+#pragma unroll
+    for (int f = 0; f < kF; ++f) {
+      const X* p = row + Keys<D, INT8>::channel(f, c);
+      if constexpr (NP == 1) {
+        q[f][0] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p));
+      } else {
+        f32x4 v[2] = {reinterpret_cast<const f32x4*>(p)[0], reinterpret_cast<const f32x4*>(p)[1]};
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+          u32x4 o;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const float x = v[s >> 1][2 * (s & 1)], y = v[s >> 1][2 * (s & 1) + 1];
+            o[s] = __builtin_amdgcn_perm(float_bits(y), float_bits(x), 0x07060302u);
+            v[s >> 1][2 * (s & 1)] = x - bits_float(float_bits(x) & 0xFFFF0000u);
+            v[s >> 1][2 * (s & 1) + 1] = y - bits_float(float_bits(y) & 0xFFFF0000u);
+          }
+          q[f][n] = __builtin_bit_cast(bf16x8, o);
+        }
+      }
+    }
+  }
+
+  f32x4 o[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] = f32x4{0, 0, 0, 0};
+  float m = kLowest, l = 0.0f;  // of query r; l of this lane's tokens
+
+  const uint32_t tiles_per_page = a.page_size / kTile;
+  const int32_t* table = a.table + (int64_t)b * a.ld_table;
+  Keys<D, INT8> k[kU];
+  Values<D, INT8> v[kU][4];
+  f32x4 ks[kU], vs[kU];
+  bool there[kU];
+
+  for (int64_t tile0 = first + wave * kU; tile0 < last; tile0 += kWaves * kU) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t tile = tile0 + u;
+      const uint32_t entry = (uint32_t)tile / tiles_per_page, slot = ((uint32_t)tile % tiles_per_page) * kTile;
+      int64_t page = tile < last ? __builtin_amdgcn_readfirstlane(table[entry]) : -1;
+      there[u] = page >= 0 && page < a.num_pages;
+      if (there[u]) {
+        const int64_t at = page * a.page_stride + h * a.head_stride + (int64_t)slot * a.token_stride;
+        // tokens before `begin` and from `end` on are not read: their lanes read the nearest one inside
+        const int lo = (int)(sp.begin - tile * kTile), hi = (int)(sp.end - 1 - tile * kTile);
+        auto inside = [&](int t) { return (uint32_t)(t < lo ? lo : (t > hi ? hi : t)); };
+        k[u].load(a.kp + at * kElem, inside(r) * a.token_stride * kElem, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[u][i].load(a.vp + at * kElem + inside(4 * c + i) * a.token_stride * kElem + r * Values<D, INT8>::kBytes);
+        if constexpr (INT8) {
+          const int64_t sc = (page * a.heads + h) * a.page_size + slot + 4 * c;
+          ks[u] = *reinterpret_cast<const f32x4*>(a.ks + sc);
+          vs[u] = *reinterpret_cast<const f32x4*>(a.vs + sc);
+        }
+      }
+    }
+    float s[kU][4];
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (!there[u]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][i] = -INFINITY;
+        continue;
+      }
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int f = 0; f < kF; ++f) {
+        const bf16x8 kf = k[u].operand(f);
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[f][n], acc, 0, 0, 0);
+      }
+      const int64_t t0 = (tile0 + u) * kTile + 4 * c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = acc[i] * a.scale;
+        if constexpr (INT8) x *= ks[u][i];
+        s[u][i] = t0 + i >= sp.begin && t0 + i < sp.end ? x : -INFINITY;
+        top = fmaxf(top, s[u][i]);
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float shrink = exp2f(m - top);
+    m = top;
+    l *= shrink;
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[e][i] *= shrink;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (!there[u]) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float p = exp2f(s[u][i] - m);
+        l += p;
+        if constexpr (INT8) p = p > 0.0f ? p * vs[u][i] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[u][i].get(e), p, o[e], 0, 0, 0);
+      }
+    }
+  }
+
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (c == 0) {
+    red_m[wave][r] = m;
+    red_l[wave][r] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red_o[wave][r][kE * (4 * c + i) + e] = o[e][i];
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < queries * D; idx += kThreads) {
+    const int j = idx / D, d = idx % D;
+    float top = red_m[0][j];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][j]);
+    float sum = 0.0f, val = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = exp2f(red_m[w][j] - top);
+      sum += f * red_l[w][j];
+      val += f * red_o[w][j][d];
+    }
+    const uint32_t head = h * a.share + q0 + j;
+    if (a.splits == 1) {
+      store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, sum > 0.0f ? val / sum : 0.0f);
+    } else {
+      const int64_t at = ((int64_t)b * a.q_heads + head) * a.splits + part;
+      a.partial[at * D + d] = val;
+      if (d == 0) {
+        float* ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * at;
+        ml[0] = top;
+        ml[1] = sum;
+      }
+    }
+  }
+}
+
+// Parts joined: one block of D threads to a query head.
+template <int D, typename X>
+__global__ __launch_bounds__(D) void join_kernel(Args a) {
+  const uint32_t b = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
+  const Span sp = span_of(a, b);
+  int64_t parts = (sp.last - sp.first + sp.per_part - 1) / sp.per_part;
+  if (parts < 1) parts = 1;
+  const int64_t at = (int64_t)blockIdx.x * a.splits;
+  const float* ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * at;
+  const float* val = a.partial + at * D + threadIdx.x;
+  float m = kLowest, l = 0.0f, o = 0.0f;
+  for (int64_t p = 0; p < parts; ++p) {
+    const float top = fmaxf(m, ml[2 * p]), f = exp2f(m - top), g = exp2f(ml[2 * p] - top);
+    l = l * f + ml[2 * p + 1] * g;
+    o = o * f + val[p * D] * g;
+    m = top;
+  }
+  store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + threadIdx.x, l > 0.0f ? o / l : 0.0f);
+}
+
+template <int D, typename X, bool INT8>
+hipError_t launch(const Args& a, hipStream_t st) {
+  attention_kernel<D, X, INT8><<<a.B * a.heads * a.q_tiles * a.splits, kThreads, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  join_kernel<D, X><<<a.B * a.q_heads, D, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_paged_attention(const AttentionArgs& in, hipStream_t st) {
+  const qv_kv_cache& c = in.cache;
+  Args a = {};
+  a.q = in.Q.data;
+  a.o = const_cast<void*>(in.O.data);
+  a.kp = static_cast<const char*>(c.k_pages);
+  a.vp = static_cast<const char*>(c.v_pages);
+  a.ks = c.k_scale;
+  a.vs = c.v_scale;
+  a.table = in.page_table;
+  a.lens = in.lens;
+  a.partial = in.partial;
+  a.q_ts = in.Q.token_stride;
+  a.q_hs = in.Q.head_stride;
+  a.o_ts = in.O.token_stride;
+  a.o_hs = in.O.head_stride;
+  a.page_stride = c.page_stride;
+  a.head_stride = c.head_stride;
+  a.ld_table = in.ld_table;
+  a.num_pages = c.num_pages;
+  a.capacity = in.max_pages * c.page_size;
+  a.window = in.window;
+  a.B = (uint32_t)in.B;
+  a.heads = (uint32_t)c.heads;
+  a.q_heads = (uint32_t)in.q_heads;
+  a.share = (uint32_t)(in.q_heads / c.heads);
+  a.q_tiles = (a.share + kTile - 1) / kTile;
+  a.splits = (uint32_t)paged_attention_splits(in.B, in.q_heads, c.heads, a.capacity);
+  a.token_stride = (uint32_t)c.token_stride;
+  a.page_size = (uint32_t)c.page_size;
+  a.scale = in.scale * kLog2e;
+  const bool q8 = c.dtype == QV_KV_INT8;
+  if (c.head_dim == 64) {
+    if (in.bf16) return q8 ? launch<64, __hip_bfloat16, true>(a, st) : launch<64, __hip_bfloat16, false>(a, st);
+    return q8 ? launch<64, float, true>(a, st) : launch<64, float, false>(a, st);
+  }
+  if (in.bf16) return q8 ? launch<128, __hip_bfloat16, true>(a, st) : launch<128, __hip_bfloat16, false>(a, st);
+  return q8 ? launch<128, float, true>(a, st) : launch<128, float, false>(a, st);
+}
+
+}  // namespace qv

@@ -1,0 +1,624 @@
+"""The single-token entry points against plain 64-bit implementations of their formulas.
+
+Tolerances, with u = 2^-24 (fp32's rounding error) and 2^-8 that of bf16 (8 significant bits):
+
+* Few-row linear.  |s x| stands for the 2-norm over k of w_scale[n][g(k)] * x[m][k].  A window of 128 codes is
+  summed with its codes raised to [16, 31], in fp32; a partial sum's rounding errors are random and below
+  31 u |x_window| times the root of about 48 roundings, so a result's error has a deviation below
+  31 * sqrt(48) / sqrt(3) u |s x| = 124 u |s x|.  Elements are held to six deviations (744 u), the whole result
+  (2-norm over 2-norm of |s x|) to one.  bf16 results with rows that were not bf16 to begin with take the rows
+  in two pieces: 2^-16 of every x more, at most 8 * 2^-16 |s x| since |q| <= 8 and errors do not add up in
+  phase; and round once, 2^-8 |y|.  The rotation adds log2 K <= 12 roundings to every x: 8 * 12 u |s x|.
+  GELU's slope is below 1.13 and its own evaluation is good to 8 u |y|.
+* Attention.  A score below 17 (in bits) is rounded about four times, 4 * 17 u, exp2 and sums add a few u:
+  1e-5 sum_t p_t |v_t| in all, plus 2^-8 |o| for bf16.
+* Append: the formula evaluated step by step in fp32 gives the same bits; against 64 bits a bf16 value is
+  off by its rounding and three fp32 roundings of terms up to |a| + |b|."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import oracle  # noqa: E402
+from guard import check_guard, guarded_output  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+U, BF = 2.0 ** -24, 2.0 ** -8
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def qv():
+    import bit_ptq_reconstruction_amd as m
+
+    m.lib()
+    return m
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return torch.device("cuda:0")
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+# ------------------------------------------------------------------------------------- few-row linears
+
+def random_weights(N, K, group, g):
+    q = torch.randint(-8, 8, (N, K), generator=g, dtype=torch.int8)
+    packed = (q[:, 0::2] & 15 | q[:, 1::2] << 4).view(torch.uint8).contiguous()
+    ws = 0.002 + 0.02 * torch.rand((N, K // group), generator=g)
+    return q, packed, ws
+
+
+def hadamard64(K):
+    return torch.from_numpy(oracle.hadamard(K).astype(np.float64))
+
+
+def expected(x, q, ws, group, bias, gelu):
+    """(y, |s x|) in 64 bits."""
+    w = q.double() * ws.double().repeat_interleave(group, 1)
+    y = x @ w.t()
+    sx = ((x ** 2) @ (ws.double().repeat_interleave(group, 1) ** 2).t()).sqrt()
+    if bias is not None:
+        y = y + bias.double()
+    return (y * torch.special.ndtr(y) if gelu else y), sx
+
+
+def check_linear(Y, y, sx, x_type, y_type, rotated, gelu, label):
+    err = (Y.double().cpu() - y).abs()
+    slope, own = (1.13, 8 * U) if gelu else (1.0, U)
+    extra = 96 * U if rotated else 0.0
+    two = 8 * 2.0 ** -16 if y_type == "bf16" and (rotated or x_type == "fp32") else 0.0
+    tol = slope * (744 * U + extra + two) * sx + own * y.abs() + (BF * 1.01 * y.abs() + 1e-38 if y_type == "bf16" else 0)
+    worst = (err / tol.clamp(min=1e-300)).max().item() if err.numel() else 0.0
+    assert worst <= 1.0, f"{label}: {worst:.2f} of the bound"
+    whole = err.norm().item() / sx.norm().item()
+    most = slope * (124 * U + extra + two) + (own + (BF if y_type == "bf16" else 0)) * y.norm().item() / sx.norm().item()
+    assert whole <= most, f"{label}: {whole:.2e} over {most:.2e}"
+
+
+GEMV = [  # M, K, N, group, x, y, bias, gelu, padding of the rows of X and Y
+    (1, 128, 1, 128, "bf16", "bf16", False, False, 0, 0),
+    (1, 1024, 1024, 128, "bf16", "bf16", False, False, 0, 0),
+    (2, 256, 15, 256, "fp32", "fp32", True, False, 4, 1),
+    (3, 384, 16, 384, "fp32", "bf16", True, True, 0, 3),
+    (4, 640, 17, 128, "bf16", "fp32", False, True, 8, 0),
+    (5, 1152, 63, 1152, "bf16", "bf16", True, True, 0, 5),
+    (7, 512, 130, 512, "fp32", "fp32", False, False, 8, 0),
+    (16, 2048, 257, 128, "bf16", "bf16", True, False, 0, 0),
+    (17, 1024, 33, 256, "bf16", "bf16", False, False, 16, 7),
+    (33, 4096, 100, 512, "fp32", "fp32", True, False, 0, 1),
+    (1, 65536, 40, 512, "bf16", "fp32", False, False, 0, 0),
+    (16, 8192, 6000, 128, "bf16", "bf16", False, False, 0, 0),
+    (1, 8192, 20001, 8192, "fp32", "bf16", False, False, 0, 0),
+    (64, 256, 333, 128, "fp32", "bf16", False, False, 0, 0),
+]
+
+
+@pytest.mark.parametrize("M,K,N,group,xt,yt,bias,gelu,padx,pady", GEMV)
+def test_gemv(qv, dev, M, K, N, group, xt, yt, bias, gelu, padx, pady):
+    g = gen(M * 1000003 + K * 31 + N)
+    q, packed, ws = random_weights(N, K, group, g)
+    X = torch.full((M, K + padx), float("nan"), dtype=DT[xt])
+    X[:, :K] = torch.randn((M, K), generator=g)
+    X[:, torch.randint(K, (3,), generator=g)] *= 30.0
+    b = torch.randn(N, generator=g) if bias else None
+    Xd = X.to(dev)[:, :K]
+    full, Y = guarded_output(M, N, DT[yt], dev, pady)
+    qv.qv_w4a16_gemv(Xd, packed.to(dev), ws.to(dev), group, None if b is None else b.to(dev), Y,
+                     qv.QV_EPI_GELU if gelu else qv.QV_EPI_NONE)
+    torch.cuda.synchronize()
+    check_guard(full, M, N)
+    y, sx = expected(X[:, :K].double(), q, ws, group, b, gelu)
+    check_linear(Y, y, sx, xt, yt, False, gelu, f"gemv {M}x{K}x{N}")
+
+
+@pytest.mark.parametrize("M,K,N,group,xt,yt,smooth,gelu,padx", [
+    (1, 1024, 1024, 128, "bf16", "bf16", True, False, 0), (1, 4096, 100, 256, "bf16", "bf16", False, False, 0),
+    (2, 1024, 37, 1024, "fp32", "fp32", True, True, 4), (3, 4096, 1024, 512, "bf16", "fp32", True, False, 8),
+    (4, 1024, 65, 512, "bf16", "bf16", True, False, 0), (5, 1024, 129, 256, "bf16", "bf16", False, True, 0),
+    (7, 4096, 50, 4096, "fp32", "bf16", True, False, 0), (13, 1024, 4099, 1024, "fp32", "fp32", True, True, 0),
+    (16, 4096, 300, 128, "bf16", "bf16", True, False, 0), (35, 1024, 64, 128, "bf16", "bf16", True, False, 0),
+])
+def test_linear(qv, dev, M, K, N, group, xt, yt, smooth, gelu, padx):
+    g = gen(M * 7919 + K + N)
+    q, packed, ws = random_weights(N, K, group, g)
+    X = torch.full((M, K + padx), float("nan"), dtype=DT[xt])
+    X[:, :K] = torch.randn((M, K), generator=g)
+    X[:, torch.randint(K, (3,), generator=g)] *= 30.0
+    inv = 0.25 + torch.rand(K, generator=g) if smooth else None
+    work = torch.full((qv.qv_w4a16_linear_workspace_size(M, K) + 256,), 0xFF, dtype=torch.uint8, device=dev)
+    full, Y = guarded_output(M, N, DT[yt], dev, 3)
+    scale = ws[:, 0].contiguous() if group == K else ws
+    qv.qv_w4a16_linear(X.to(dev)[:, :K], None if inv is None else inv.to(dev), packed.to(dev), scale.to(dev), group,
+                       None, Y, work[:-256], qv.QV_EPI_GELU if gelu else qv.QV_EPI_NONE)
+    torch.cuda.synchronize()
+    check_guard(full, M, N)
+    assert bool((work[-256:] == 0xFF).all())
+    x = X[:, :K].double() @ hadamard64(K) / math.sqrt(K)
+    if inv is not None:
+        x = x * inv.double()
+    y, sx = expected(x, q, ws, group, None, gelu)
+    check_linear(Y, y, sx, xt, yt, True, gelu, f"linear {M}x{K}x{N}")
+
+
+@pytest.mark.parametrize("group", [128, 1024])
+def test_linear_takes_packed_weights(qv, dev, group):
+    """Weights packed by the library's own offline calls, against the dequantized codes they hold."""
+    M, K, N = 6, 1024, 256
+    g = gen(5)
+    W = 0.02 * torch.randn((N, K), generator=g)
+    s = 0.5 + torch.rand(K, generator=g)
+    Wq = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
+    ws = torch.empty((N, K // group) if group < K else (N,), device=dev)
+    if group < K:
+        qv.qv_pack_weights_grouped(W.to(dev), s.to(dev), group, Wq, ws)
+    else:
+        qv.qv_pack_weights(W.to(dev), s.to(dev), Wq, ws)
+    X = torch.randn((M, K), generator=g)
+    Y = torch.empty((M, N), device=dev)
+    work = torch.empty(qv.qv_w4a16_linear_workspace_size(M, K), dtype=torch.uint8, device=dev)
+    qv.qv_w4a16_linear(X.to(dev), (1 / s).to(dev), Wq, ws, group, None, Y, work)
+    q = torch.from_numpy(oracle.unpack_int4(Wq.cpu().numpy()).astype(np.int8))
+    x = X.double() @ hadamard64(K) / math.sqrt(K) * (1 / s).double()
+    y, sx = expected(x, q, ws.cpu().view(N, -1), group, None, False)
+    check_linear(Y, y, sx, "fp32", "fp32", True, False, "packed")
+    # against the layer itself: a code is off by a twelfth of a squared step, so the whole by |step x| / sqrt(12)
+    # (N * M = 1536 values, a deviation of about 2 % on the norm; half as much again is allowed)
+    step = sx.norm().item() / math.sqrt(12)
+    assert (Y.double().cpu() - X.double() @ W.double().t()).norm().item() <= 1.5 * step
+
+
+def test_linear_codes_and_zero_rows(qv, dev):
+    """Every code against a single one among zeros is exact; zero rows and zero scales give zeros."""
+    K, N = 128, 16
+    q = (torch.arange(N, dtype=torch.int8) - 8)[:, None].repeat(1, K)
+    packed = (q[:, 0::2] & 15 | q[:, 1::2] << 4).view(torch.uint8).contiguous().to(dev)
+    X = torch.zeros((5, K))
+    X[1, 0], X[2, 77], X[3, 127] = 1.0, -3.0, 2.0 ** -100
+    ws = torch.full((N, 1), 0.5)
+    Y = torch.empty((5, N), device=dev)
+    qv.qv_w4a16_gemv(X.to(dev), packed, ws.to(dev), K, None, Y)
+    expect = X.sum(1, keepdim=True) * 0.5 * (torch.arange(N) - 8)
+    assert torch.equal(Y.cpu(), expect)
+    qv.qv_w4a16_gemv(X.to(dev), packed, torch.zeros_like(ws).to(dev), K, None, Y)
+    assert bool((Y == 0).all())
+
+
+def test_empty_calls(qv, dev):
+    e = lambda *s, **k: torch.empty(s, device=dev, **k)
+    qv.qv_w4a16_gemv(e(0, 256), e(8, 128, dtype=torch.uint8), e(8, 2), 128, None, e(0, 8))
+    qv.qv_w4a16_gemv(e(3, 256), e(0, 128, dtype=torch.uint8), e(0, 2), 128, None, e(3, 0))
+    c = make_cache(qv, dev, 2, 2, 16, 64, "bf16", 0)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+    before = c.k_pages.clone()
+    qv.qv_kv_append(c, i(1, 2), i(0), i(0), e(0, 2, 64), e(0, 2, 64))
+    assert torch.equal(c.k_pages.view(torch.int16), before.view(torch.int16))
+    qv.qv_paged_attention(e(0, 4, 64), c, i(0, 2), i(0), e(0, 4, 64), e(256, dtype=torch.uint8))
+
+
+# ----------------------------------------------------------------------------------------- paged cache
+
+def make_cache(qv, dev, pages, heads, size, dim, kind, seed, order="head"):
+    """A cache that holds NaN (int8: codes under NaN scales) everywhere."""
+    shape = (pages, heads, size, dim) if order == "head" else (pages, size, heads, dim)
+    if kind == "bf16":
+        k, v = (torch.full(shape, float("nan"), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        ks = vs = None
+    else:
+        k, v = (torch.full(shape, 77, dtype=torch.int8, device=dev) for _ in range(2))
+        ks, vs = (torch.full((pages, heads, size), float("nan"), device=dev) for _ in range(2))
+    if order != "head":
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+    return qv.QVKVCache(k, v, ks, vs)
+
+
+def fill(cache, table, lens, g):
+    """Random tokens at places [0, lens[b]) of every sequence; returns their exact values [b] -> (k, v) [t, H, D]."""
+    out = []
+    for b, n in enumerate(lens):
+        t = torch.arange(n)
+        page, slot = table[b, t // cache.page_size].long(), t % cache.page_size
+        keep = page >= 0
+        pair = []
+        for pages, scales in ((cache.k_pages, cache.k_scale), (cache.v_pages, cache.v_scale)):
+            x = torch.randn((n, cache.heads, cache.head_dim), generator=g)
+            if scales is None:
+                x = x.to(torch.bfloat16)
+                val = x.double()
+            else:
+                s = 0.004 + 0.02 * torch.rand((n, cache.heads), generator=g)
+                x = torch.randint(-128, 128, x.shape, generator=g, dtype=torch.int8)
+                val = x.double() * s.double()[..., None]
+                scales[page[keep].to(scales.device), :, slot[keep].to(scales.device)] = s[keep].to(scales.device)
+            pages[page[keep].to(pages.device), :, slot[keep].to(pages.device)] = x[keep].to(pages.device)
+            pair.append(val)
+        out.append((pair[0], pair[1], keep))
+    return out
+
+
+def shuffled_table(lens, size, g, extra=0, spare=2):
+    need = [-(-n // size) for n in lens]
+    pool = torch.randperm(sum(need) + spare, generator=g, dtype=torch.int32)
+    table = torch.full((len(lens), max(need + [0]) + extra), -7, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = pool[at:at + n]
+        at += n
+    return table, len(pool)
+
+
+def attention64(Q, kv, lens, window, scale):
+    """(o, sum p |v|) [B, Hq, D] in 64 bits."""
+    B, Hq, D = Q.shape
+    o, mag = torch.zeros((B, Hq, D), dtype=torch.float64), torch.zeros((B, Hq, D), dtype=torch.float64)
+    for b, n in enumerate(lens):
+        k, v, keep = kv[b]
+        t = torch.arange(n)
+        use = keep & ((t >= n - window) if window else torch.ones(n, dtype=torch.bool))
+        if not bool(use.any()):
+            continue
+        k, v = k[use], v[use]
+        H = k.shape[1]
+        s = Q[b].double().view(H, Hq // H, D) @ k.permute(1, 2, 0) * scale
+        p = torch.softmax(s, -1)
+        o[b] = (p @ v.transpose(0, 1)).view(Hq, D)
+        mag[b] = (p @ v.abs().transpose(0, 1)).view(Hq, D)
+    return o, mag
+
+
+def check_attention(O, o, mag, kind, label):
+    err = (O.double().cpu() - o).abs()
+    tol = 1e-5 * mag + (BF * 1.01 * o.abs() + 1e-38 if kind == "bf16" else 0)
+    worst = (err / tol.clamp(min=1e-300)).max().item()
+    assert worst <= 1.0, f"{label}: {worst:.2f} of the bound"
+
+
+def attend(qv, dev, Q, cache, table, lens, window=0, scale=None, pad=0):
+    """O with guard rows behind it and a workspace with guard bytes."""
+    B, Hq, D = Q.shape
+    full = torch.full((B + 3, Hq, D + pad), float("nan"), dtype=Q.dtype, device=dev)
+    O = full[:B, :, :D]
+    size = qv.qv_paged_attention_workspace_size(B, Hq, cache.heads, D, table.shape[1] * cache.page_size)
+    work = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device=dev)
+    qv.qv_paged_attention(Q, cache, table, torch.tensor(lens, dtype=torch.int32, device=dev), O, work[:size], scale,
+                          window)
+    torch.cuda.synchronize()
+    assert bool((work[size:] == 0xFF).all())
+    assert bool(torch.isnan(full[B:].float()).all()) and bool(torch.isnan(full[:, :, D:].float()).all())
+    return O
+
+
+ATTEND = [  # lens, heads, share, dim, page, window, x, cache, order
+    ([1], 1, 1, 64, 16, 0, "bf16", "bf16", "head"),
+    ([0, 1, 2, 15, 16, 17, 31, 32, 33], 2, 1, 64, 16, 0, "bf16", "bf16", "head"),
+    ([47, 0, 200, 129], 3, 5, 128, 48, 0, "bf16", "bf16", "head"),
+    ([63, 64, 65, 127, 128], 2, 4, 128, 64, 0, "fp32", "bf16", "slot"),
+    ([100, 300], 1, 17, 64, 32, 0, "bf16", "bf16", "head"),
+    ([77, 500], 1, 33, 128, 16, 0, "fp32", "int8", "slot"),
+    ([1, 16, 40, 255], 4, 8, 128, 16, 0, "bf16", "int8", "head"),
+    ([90, 33, 0], 3, 3, 64, 128, 0, "bf16", "int8", "slot"),
+    ([700, 5, 64, 2000], 2, 2, 64, 16, 37, "fp32", "bf16", "head"),
+    ([700, 1374, 1], 2, 1, 128, 32, 512, "bf16", "int8", "head"),
+    ([3000], 16, 1, 64, 16, 0, "bf16", "bf16", "head"),
+    ([5003, 11, 2500], 2, 7, 128, 64, 0, "fp32", "bf16", "head"),
+    ([20011], 1, 8, 128, 256, 0, "bf16", "int8", "head"),
+]
+
+
+@pytest.mark.parametrize("lens,heads,share,dim,page,window,xt,kind,order", ATTEND)
+def test_attention(qv, dev, lens, heads, share, dim, page, window, xt, kind, order):
+    g = gen(sum(lens) + heads + share + dim)
+    table, pages = shuffled_table(lens, page, g, extra=len(lens) % 3)
+    cache = make_cache(qv, dev, pages, heads, page, dim, kind, 0, order)
+    kv = fill(cache, table, lens, g)
+    Q = torch.randn((len(lens), heads * share, dim), generator=g).to(DT[xt])
+    wide = torch.full((len(lens), heads * share, 3 * dim), float("nan"), dtype=DT[xt])  # a slice of a packed tensor
+    wide[:, :, dim:2 * dim] = Q
+    O = attend(qv, dev, wide.to(dev)[:, :, dim:2 * dim], cache, table.to(dev), lens, window, None, 8)
+    o, mag = attention64(Q, kv, lens, window, dim ** -0.5)
+    check_attention(O, o, mag, xt, f"{lens} {kind}")
+    assert bool((O[[n == 0 for n in lens]] == 0).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_attention_pages_given_back(qv, dev, kind):
+    """Tokens on a page outside the cache do not take part, at the start, in the middle, at the end, everywhere."""
+    lens, size = [400, 400, 390, 64, 17], 16
+    g = gen(3)
+    table, pages = shuffled_table(lens, size, g)
+    table[0, :9] = -1
+    table[1, 5], table[1, 11:14], table[1, 24] = pages, 1 << 30, -(1 << 31)
+    table[2, ::2] = -1
+    table[3, :] = -1
+    cache = make_cache(qv, dev, pages, 2, size, 64, kind, 0)
+    bad = (table < 0) | (table >= pages)
+    safe = torch.where(bad, torch.full_like(table, -1), table)
+    kv = fill(cache, safe, lens, g)
+    Q = torch.randn((5, 4, 64), generator=g)
+    O = attend(qv, dev, Q.to(dev), cache, table.to(dev), lens)
+    o, mag = attention64(Q, kv, lens, 0, 0.125)
+    check_attention(O, o, mag, "fp32", "given back")
+    assert bool((O[3] == 0).all())
+
+
+def test_attention_lengths_are_cut(qv, dev):
+    """A length past the page table counts what the table holds, a negative one is empty; scale and a table that is
+    a view of a wider one are taken as given."""
+    g = gen(8)
+    table, pages = shuffled_table([64, 64, 64], 16, g)
+    cache = make_cache(qv, dev, pages, 1, 16, 64, "bf16", 0)
+    kv = fill(cache, table, [64, 64, 64], g)
+    Q = torch.randn((3, 2, 64), generator=g)
+    wide = torch.full((3, 9), 1 << 20, dtype=torch.int32)
+    wide[:, 3:7] = table
+    O = attend(qv, dev, Q.to(dev), cache, wide.to(dev)[:, 3:7], [64, 1 << 30, -5], 0, 0.3)
+    o, mag = attention64(Q, kv, [64, 64, 64], 0, 0.3)
+    check_attention(O[:2], o[:2], mag[:2], "fp32", "cut")
+    assert bool((O[2] == 0).all())
+    O = attend(qv, dev, Q.to(dev), cache, table.to(dev)[:, :0], [64, 1, 0])
+    assert bool((O == 0).all())
+
+
+def test_attention_extreme_scores(qv, dev):
+    """One score far above or below the others, and scores that all lie far from zero."""
+    g = gen(4)
+    lens = [600, 600, 600]
+    table, pages = shuffled_table(lens, 32, g)
+    cache = make_cache(qv, dev, pages, 1, 32, 128, "bf16", 0)
+    kv = fill(cache, table, lens, g)
+    for b, (t, f) in enumerate(((599, 40.0), (0, -40.0), (300, 0.0))):
+        page, slot = int(table[b, t // 32]), t % 32
+        x = torch.full((1, 128), f, dtype=torch.bfloat16)
+        cache.k_pages[page, :, slot] = x.to(dev)
+        kv[b][0][t] = x.double()
+    Q = torch.ones((3, 1, 128))
+    Q[2] = -30.0 + torch.randn((1, 128), generator=g)
+    O = attend(qv, dev, Q.to(dev), cache, table.to(dev), lens)
+    o, _ = attention64(Q, kv, lens, 0, 128 ** -0.5)
+    # scores reach 450 (650 bits) and, for the third sequence, about 100 (150 bits): 4 * 650 u on their exponents
+    err = (O.double().cpu() - o).abs().max(dim=2)[0].max(dim=1)[0]
+    assert bool((err <= 4 * 650 * U * 5).all()), err
+
+
+def test_attention_far_pages(qv, dev):
+    """Pages whose offset passes 2^32 elements, in either tensor."""
+    size, heads, dim = 256, 16, 128
+    pages = (1 << 32) // (size * heads * dim) + 5
+    k, v = (torch.empty((pages, heads, size, dim), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    cache = qv.QVKVCache(k, v)
+    g = gen(1)
+    lens = [300, 513]
+    table = torch.tensor([[pages - 1, 0, -1], [pages - 3, 1, pages - 2]], dtype=torch.int32)
+    T = sum(lens)
+    seq = torch.repeat_interleave(torch.arange(2, dtype=torch.int32), torch.tensor(lens))
+    index = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens])
+    K, V = (torch.randn((T, heads, dim), generator=g).to(torch.bfloat16) for _ in range(2))
+    qv.qv_kv_append(cache, table.to(dev), seq.to(dev), index.to(dev), K.to(dev), V.to(dev))
+    kv = [(K[seq == b].double(), V[seq == b].double(), torch.ones(n, dtype=torch.bool)) for b, n in enumerate(lens)]
+    Q = torch.randn((2, heads, dim), generator=g).to(torch.bfloat16)
+    O = attend(qv, dev, Q.to(dev), cache, table.to(dev), lens)
+    o, mag = attention64(Q, kv, lens, 0, dim ** -0.5)
+    check_attention(O, o, mag, "bf16", "far pages")
+
+
+# --------------------------------------------------------------------------------------------- append
+
+def turn32(x, cos, sin, position, axes):
+    """The rotation in fp32 on the CPU, one rounding to each product and sum."""
+    T, H, D = x.shape
+    x = x.float().view(T, H, axes, 2, -1)
+    c, s = cos[position.long()][:, None], sin[position.long()][:, None]
+    a, b = x[:, :, :, 0], x[:, :, :, 1]
+    return torch.stack((a * c - b * s, b * c + a * s), 3).reshape(T, H, D)
+
+
+def codes32(x):
+    scale = x.abs().amax(-1) / torch.tensor(127.0)
+    scale = torch.where(scale >= 2.0 ** -126, scale, torch.zeros_like(scale))
+    q = torch.where(scale[..., None] > 0, (x / scale[..., None]).round().clamp(-128, 127), torch.zeros_like(x))
+    return q.to(torch.int8), scale
+
+
+APPEND = [  # tokens of each sequence, tokens before, heads, q_heads, dim, axes, page, x, cache, order
+    ([1], [0], 1, 1, 64, 1, 16, "bf16", "bf16", "head"),
+    ([1, 1, 1, 1, 1], [0, 15, 16, 17, 100], 2, 6, 128, 1, 16, "bf16", "bf16", "head"),
+    ([37, 1, 0, 64], [3, 0, 9, 16], 3, 3, 64, 2, 16, "fp32", "bf16", "slot"),
+    ([100, 33], [0, 31], 4, 16, 128, 2, 48, "bf16", "int8", "head"),
+    ([19, 200, 1], [1, 0, 63], 1, 5, 64, 1, 64, "fp32", "int8", "slot"),
+    ([1374], [0], 16, 16, 64, 2, 64, "bf16", "bf16", "head"),
+]
+
+
+@pytest.mark.parametrize("new,before,heads,q_heads,dim,axes,page,xt,kind,order", APPEND)
+@pytest.mark.parametrize("rotate", [True, False])
+def test_append(qv, dev, new, before, heads, q_heads, dim, axes, page, xt, kind, order, rotate):
+    g = gen(sum(new) * 13 + heads + dim)
+    table, pages = shuffled_table([a + b for a, b in zip(new, before)], page, g)
+    cache = make_cache(qv, dev, pages, heads, page, dim, kind, 0, order)
+    old = [None if t is None else t.clone() for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+    T = sum(new)
+    seq = torch.cat([torch.full((n,), b, dtype=torch.int32) for b, n in enumerate(new)])
+    index = torch.cat([torch.arange(n, dtype=torch.int32) + p for n, p in zip(new, before)])
+    mix = torch.randperm(T, generator=g)  # tokens in any order
+    seq, index = seq[mix], index[mix]
+    places = 211 if axes == 2 else int(index.max()) + 1
+    position = torch.randint(places, (T, axes), generator=g, dtype=torch.int32) if axes == 2 else index[:, None].contiguous()
+    w = dim // axes
+    angle = torch.arange(places)[:, None] * 100.0 ** (-torch.arange(0, w, 2) / w)
+    cos, sin = angle.cos(), angle.sin()
+    packed = torch.randn((T, q_heads + 2 * heads, dim), generator=g).to(DT[xt])
+    Q, K, V = packed.split((q_heads, heads, heads), 1)
+    pd = packed.to(dev)
+    Qd, Kd, Vd = pd.split((q_heads, heads, heads), 1)
+    out = torch.full((T + 2, q_heads, dim), float("nan"), dtype=DT[xt], device=dev)
+    d = lambda t: t.to(dev)
+    rot = dict(cos=d(cos), sin=d(sin), position=None if axes == 1 and T % 2 else d(position)) if rotate else {}
+    qv.qv_kv_append(cache, d(table), d(seq), d(index), Kd, Vd, Q=Qd, Q_out=out[:T], **rot)
+    torch.cuda.synchronize()
+    assert torch.equal(pd.cpu(), packed)
+    assert bool(torch.isnan(out[T:].float()).all())
+
+    k32, q32 = ((turn32(x, cos, sin, position, axes) if rotate else x.float()) for x in (K, Q))
+    assert torch.equal(out[:T].cpu(), q32.to(DT[xt]))
+    pg, slot = table[seq.long(), (index // page).long()].long(), (index % page).long()
+    for pages_, scales, kept, kept_s, x in ((cache.k_pages, cache.k_scale, old[0], old[2], k32),
+                                            (cache.v_pages, cache.v_scale, old[1], old[3], V.float())):
+        expect, expect_s = kept.cpu(), None if kept_s is None else kept_s.cpu()
+        if kind == "bf16":
+            expect[pg, :, slot] = x.to(torch.bfloat16)
+            assert torch.equal(pages_.cpu().contiguous().view(torch.int16), expect.contiguous().view(torch.int16))
+        else:
+            expect[pg, :, slot], expect_s[pg, :, slot] = codes32(x)
+            assert torch.equal(pages_.cpu(), expect)
+            assert torch.equal(scales.cpu().view(torch.int32), expect_s.view(torch.int32))
+    if rotate:  # against 64 bits
+        z = K.double().view(T, heads, axes, 2, -1)
+        c, s = (t.double()[position.long()][:, None] for t in (cos, sin))
+        a, b = z[:, :, :, 0], z[:, :, :, 1]
+        k64 = torch.stack((a * c - b * s, b * c + a * s), 3).reshape(T, heads, dim)
+        terms = (a.abs() + b.abs())[:, :, :, None].expand(-1, -1, -1, 2, -1).reshape(T, heads, dim)
+        got = cache.k_pages.cpu()[pg, :, slot].double()
+        if kind == "bf16":
+            assert bool(((got - k64).abs() <= BF * 1.01 * k64.abs() + 3 * U * terms).all())
+        else:
+            sc = cache.k_scale.cpu()[pg, :, slot].double()[..., None]
+            assert bool(((got * sc - k64).abs() <= sc * 0.5001 + 3 * U * terms).all())
+
+
+def test_append_out_of_place_tokens(qv, dev):
+    """Tokens whose sequence, place, page or position lies outside are not stored; a position outside the tables
+    gives NaN queries, the others theirs."""
+    g = gen(6)
+    table = torch.tensor([[1, -1, 9], [0, 2, 3]], dtype=torch.int32)
+    cache = make_cache(qv, dev, 4, 2, 16, 64, "bf16", 0)
+    seq = torch.tensor([0, 0, 0, 1, -1, 2, 1, 1, 1, 0], dtype=torch.int32)
+    index = torch.tensor([0, 17, 33, 47, 3, 3, 48, -1, 20, 5], dtype=torch.int32)
+    position = torch.tensor([0, 1, 2, 3, 4, 5, 6, 7, 8, 9], dtype=torch.int32)[:, None].contiguous()
+    position[8], position[9] = 10, -1
+    stored = [True, False, False, True, False, False, False, False, False, False]
+    T = len(seq)
+    K, V, Q = (torch.randn((T, 2, 64), generator=g) for _ in range(3))
+    angle = torch.arange(10)[:, None] * 10.0 ** (-torch.arange(32) / 32)
+    Qd = Q.to(dev)
+    qv.qv_kv_append(cache, table.to(dev), seq.to(dev), index.to(dev), K.to(dev), V.to(dev), angle.cos().to(dev),
+                    angle.sin().to(dev), position.to(dev), Qd, Qd)  # queries in place
+    torch.cuda.synchronize()
+    count = 0
+    for t in range(T):
+        if stored[t]:
+            page, slot = int(table[seq[t], index[t] // 16]), int(index[t] % 16)
+            assert torch.equal(cache.v_pages[page, :, slot].cpu(), V[t].to(torch.bfloat16))
+            count += 1
+    assert int((~torch.isnan(cache.v_pages.float())).sum()) == count * 2 * 64
+    assert int((~torch.isnan(cache.k_pages.float())).sum()) == count * 2 * 64
+    expect = turn32(Q, angle.cos(), angle.sin(), position.clamp(0, 9), 1)
+    assert torch.equal(Qd[:8].cpu(), expect[:8]) and bool(torch.isnan(Qd[8:]).all())
+
+
+def test_append_int8_special_rows(qv, dev):
+    """Zero and subnormal rows get scale 0 and zero codes, ties go to even, a row of one value becomes 127."""
+    cache = make_cache(qv, dev, 1, 1, 16, 64, "int8", 0)
+    V = torch.zeros((5, 1, 64))
+    V[1] = 1e-41
+    V[2, 0, :6] = torch.tensor([127.0, 0.5, 1.5, 2.5, -0.5, -1.5])
+    V[3] = -3.7
+    V[4, 0, 5] = 3.3e38
+    i = torch.arange(5, dtype=torch.int32, device=dev)
+    table = torch.zeros((1, 1), dtype=torch.int32, device=dev)
+    qv.qv_kv_append(cache, table, torch.zeros_like(i), i, V.to(dev), V.to(dev))
+    s, q = cache.v_scale[0, 0, :5].cpu(), cache.v_pages[0, 0, :5].cpu()
+    assert s[0] == 0 and s[1] == 0 and s[2] == 1 and not bool(q[:2].any())
+    assert q[2, :6].tolist() == [127, 0, 2, 2, 0, -2]
+    assert bool((q[3] == -127).all()) and q[4, 5] == 127 and int(q[4].abs().sum()) == 127
+
+
+# ------------------------------------------------------------------------------------- streams, graphs
+
+class Step:
+    """Projection, append and attention of one new token of each sequence, as a serving loop calls them."""
+
+    def __init__(self, qv, dev, kind, seed=0):
+        self.qv, g = qv, gen(seed)
+        self.B, self.H, self.D, page = 3, 16, 64, 16
+        self.lens = torch.tensor([40, 1, 700], dtype=torch.int32, device=dev)
+        table, pages = shuffled_table([48, 48, 760], page, g)
+        self.table = table.to(dev)
+        self.cache = make_cache(qv, dev, pages, self.H, page, self.D, kind, 0)
+        fill(self.cache, table, self.lens.tolist(), g)
+        q, packed, ws = random_weights(3 * 1024, 1024, 128, g)
+        self.Wq, self.ws = packed.to(dev), ws.to(dev)
+        self.x = torch.randn((self.B, 1024), generator=g).to(torch.bfloat16).to(dev)
+        self.qkv = torch.empty((self.B, 3, self.H, self.D), dtype=torch.bfloat16, device=dev)
+        self.q = torch.empty((self.B, self.H, self.D), dtype=torch.bfloat16, device=dev)
+        self.o = torch.empty_like(self.q)
+        angle = torch.arange(800)[:, None] * 100.0 ** (-torch.arange(32) / 32)
+        self.cos, self.sin = angle.cos().to(dev), angle.sin().to(dev)
+        e = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)
+        self.work = e(qv.qv_w4a16_linear_workspace_size(self.B, 1024))
+        self.part = e(qv.qv_paged_attention_workspace_size(self.B, self.H, self.H, self.D, table.shape[1] * page))
+
+    def __call__(self, stream=None):
+        qv = self.qv
+        qv.qv_w4a16_linear(self.x, None, self.Wq, self.ws, 128, None, self.qkv.view(self.B, -1), self.work,
+                           stream=stream)
+        qv.qv_kv_append(self.cache, self.table, None, self.lens, self.qkv[:, 1], self.qkv[:, 2], self.cos, self.sin,
+                        Q=self.qkv[:, 0], Q_out=self.q, stream=stream)
+        self.lens.add_(1)
+        qv.qv_paged_attention(self.q, self.cache, self.table, self.lens, self.o, self.part, stream=stream)
+        return self.o
+
+
+def test_step_on_another_stream(qv, dev):
+    a, b = Step(qv, dev, "bf16"), Step(qv, dev, "bf16")
+    torch.cuda.synchronize()
+    one = [a().clone() for _ in range(4)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        two = [b(stream=s).clone() for _ in range(4)]
+    torch.cuda.synchronize()
+    assert not bool(torch.isnan(one[-1].float()).any())
+    for x, y in zip(one, two):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_step_in_a_graph(qv, dev, kind):
+    """A captured step, replayed with eager work and synchronizations between, gives what eager steps give."""
+    eager, step = Step(qv, dev, kind), Step(qv, dev, kind)
+    expect = [eager().clone() for _ in range(6)]
+    first = step().clone()
+    assert torch.equal(first, expect[0])
+    graph = torch.cuda.CUDAGraph()
+    before = step.lens.clone()
+    with torch.cuda.graph(graph):
+        step()
+    step.lens.copy_(before)
+    for i in range(1, 6):
+        step.o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(step.o, expect[i]), i
+        eager.x.float().sum().item()
+
+
+def test_results_repeat(qv, dev):
+    """The same call gives the same bits."""
+    g = gen(2)
+    lens = [4000, 900]
+    table, pages = shuffled_table(lens, 16, g)
+    cache = make_cache(qv, dev, pages, 2, 16, 128, "bf16", 0)
+    fill(cache, table, lens, g)
+    Q = torch.randn((2, 8, 128), generator=g).to(dev)
+    a, b = (attend(qv, dev, Q, cache, table.to(dev), lens).clone() for _ in range(2))
+    assert torch.equal(a, b)
