@@ -9,9 +9,12 @@
 // Products run on the matrix cores, 16 rows x 16 channels x 32 codes at a time, whatever M is: one
 // v_mfma_f32_16x16x32_bf16 replaces 512 multiply-adds for 16 cycles, and the vector ALU is left with
 // the unpacking.  Both operands are exact in bf16:
-//   - a code q becomes 24 + q in [16, 31], i.e. the bits 0x4180 | (q + 8) << 3: one shift and one
-//     and-or for two codes.  The surplus 24 * sum_k x[m][k] is formed by one more MFMA against ones and
-//     taken off each group's sum.  (An offset of 136 would save nothing and cost 2.5 bits.)
+//   - with fp32 results a code is converted by itself (v_cvt_off_f32_i4 gives q / 16, and the upper halves
+//     of two are packed: 19 instructions for 8 codes).
+//   - with bf16 results a code q becomes 24 + q in [16, 31], i.e. the bits 0x4180 | (q + 8) << 3: one shift
+//     and one and-or for two codes, 9 instructions for 8.  The surplus 24 * sum_k x[m][k] is formed by one more
+//     MFMA against ones and taken off each group's sum.  The larger partial sums triple the fp32
+//     rounding error, from 3e-7 of the result to 1e-6, which a bf16 result does not show and an fp32 one does.
 //   - an activation is a sum of NP bf16 pieces (the top 16 bits, then the top 16 bits of the rest, ...):
 //     one piece is exact for bf16 rows, two keep 16 bits for rotated or fp32 rows with a bf16 result
 //     (2^-16 against the result's own 2^-9), three keep all 24 bits for fp32 results.
@@ -96,6 +99,18 @@ __device__ __forceinline__ void pieces(const Eight<float>& v, bf16x8 (&f)[NP]) {
     }
     f[p] = __builtin_bit_cast(bf16x8, o);
   }
+}
+
+// Eight codes -> q / 16 in bf16, exactly, dword s holding codes s and s + 4.
+__device__ __forceinline__ bf16x8 widen_exact(unsigned w) {
+  u32x4 o;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const float a = __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * s)));
+    const float b = __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * s + 16)));
+    o[s] = __builtin_amdgcn_perm(float_bits(b), float_bits(a), 0x07060302u);
+  }
+  return __builtin_bit_cast(bf16x8, o);
 }
 
 // Eight codes -> 24 + q in bf16, dword s holding codes s and s + 4.
@@ -186,9 +201,9 @@ struct Args {
   int gelu, y_bf16;
 };
 
-// KROT: 0: rows are read from memory as they are; else the Hadamard width K, and the block rotates
+// EXACT: fp32 results, codes converted exactly.  KROT: 0: rows are read from memory as they are; else the Hadamard width K, and the block rotates
 // its rows into LDS first.
-template <typename X, int NP, int NT, int KROT>
+template <typename X, int NP, bool EXACT, int NT, int KROT>
 __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   extern __shared__ f32x4 lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -265,11 +280,13 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
     if (win + kWaves < windows) load_weights(win + kWaves);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if constexpr (!EXACT) {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], ones, sum, 0, 0, 0);
+        for (int p = 0; p < NP; ++p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], ones, sum, 0, 0, 0);
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const bf16x8 wf = widen(wc[t][j]);
+        const bf16x8 wf = EXACT ? widen_exact(wc[t][j]) : widen(wc[t][j]);
 #pragma unroll
         for (int p = 0; p < NP; ++p) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], wf, acc[t], 0, 0, 0);
       }
@@ -277,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[t][i] += sc[t] * (acc[t][i] - 24.0f * sum[i]);
+      for (int i = 0; i < 4; ++i) y[t][i] += EXACT ? 16.0f * sc[t] * acc[t][i] : sc[t] * (acc[t][i] - 24.0f * sum[i]);
   }
 
   // Element (m, n) of tile t at [wave][t][m][n].
@@ -318,7 +335,7 @@ __global__ __launch_bounds__(K / 8) void rotate_rows_kernel(const X* __restrict_
   o[1] = p[1];
 }
 
-template <typename X, int NP, int NT, int KROT>
+template <typename X, int NP, bool EXACT, int NT, int KROT>
 hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
   const unsigned gx = (unsigned)((a.N + 16 * NT - 1) / (16 * NT));
   const int rows = (int)(a.M < kRows ? a.M : kRows);
@@ -331,16 +348,25 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
     b.x += m * a.ldx;
     b.M = a.M - m < step ? a.M - m : step;
     b.y = static_cast<char*>(a.y) + m * a.ldy * (a.y_bf16 ? 2 : 4);
-    w4a16_kernel<X, NP, NT, KROT><<<dim3(gx, (unsigned)((b.M + kRows - 1) / kRows)), kThreads, bytes, st>>>(b);
+    w4a16_kernel<X, NP, EXACT, NT, KROT><<<dim3(gx, (unsigned)((b.M + kRows - 1) / kRows)), kThreads, bytes, st>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <typename X, int NP, int KROT>
+template <typename X, int NP, bool EXACT, int KROT>
 hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
-  return launch_kernel<X, NP, 1, KROT>(a, st);
+  return launch_kernel<X, NP, EXACT, 1, KROT>(a, st);
+}
+
+// Pieces by the types: rows that are bf16 are one piece; others two or, for fp32 results, three.
+template <typename X, int KROT>
+hipError_t by_types(const Args<X>& a, hipStream_t st) {
+  if constexpr (sizeof(X) == 2 && KROT == 0)
+    return a.y_bf16 ? by_tiles<X, 1, false, KROT>(a, st) : by_tiles<X, 1, true, KROT>(a, st);
+  else
+    return a.y_bf16 ? by_tiles<X, 2, false, KROT>(a, st) : by_tiles<X, 3, true, KROT>(a, st);
 }
 
 template <typename X>
@@ -354,18 +380,13 @@ hipError_t rotate_rows(const X* x, int64_t M, int64_t K, int64_t ldx, const floa
 
 template <typename X>
 hipError_t launch(Args<X> a, bool rotate, float* rows32, hipStream_t st) {
-  if (!rotate) {
-    if constexpr (sizeof(X) == 2) return by_tiles<X, 1, 0>(a, st);
-    else return a.y_bf16 ? by_tiles<X, 2, 0>(a, st) : by_tiles<X, 3, 0>(a, st);
-  }
-  if (a.M <= 4) {
-    if (a.K == 1024) return a.y_bf16 ? by_tiles<X, 2, 1024>(a, st) : by_tiles<X, 3, 1024>(a, st);
-    if (a.M == 1) return a.y_bf16 ? by_tiles<X, 2, 4096>(a, st) : by_tiles<X, 3, 4096>(a, st);
-  }
+  if (!rotate) return by_types<X, 0>(a, st);
+  if (a.K == 1024 && a.M <= 4) return by_types<X, 1024>(a, st);
+  if (a.K == 4096 && a.M == 1) return by_types<X, 4096>(a, st);
   const hipError_t e = rotate_rows<X>(a.x, a.M, a.K, a.ldx, a.mult, rows32, st);
   if (e != hipSuccess) return e;
   const Args<float> b = {rows32, nullptr, a.wq, a.ws, a.bias, a.y, a.M, a.K, a.ldy, a.N, a.K, a.group, a.gelu, a.y_bf16};
-  return a.y_bf16 ? by_tiles<float, 2, 0>(b, st) : by_tiles<float, 3, 0>(b, st);
+  return by_types<float, 0>(b, st);
 }
 
 }  // namespace

@@ -99,11 +99,11 @@ def cache(**kw):
     f = dict(k_pages=P, v_pages=P, k_scale=P, v_scale=P, num_pages=8, heads=2, page_size=16, head_dim=64,
              page_stride=2048, head_stride=1024, token_stride=64, dtype=0)
     f.update(kw)
-    return ctypes.byref(decode._Cache(*[f[n] for n, _ in decode._Cache._fields_]))
+    return ctypes.byref(decode.QVKVCacheStruct(*[f[n] for n, _ in decode.QVKVCacheStruct._fields_]))
 
 
 def heads(data=P, ts=128, hs=64):
-    return ctypes.byref(decode._Heads(data, ts, hs))
+    return ctypes.byref(decode.QVHeadsStruct(data, ts, hs))
 
 
 def append(L, cache_=None, table=P, seqs=3, pages=4, ld=4, seq=P, index=P, T=5, K=0, V=0, xt=BF16, cos=P, sin=P,
