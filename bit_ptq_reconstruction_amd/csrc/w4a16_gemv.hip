@@ -28,6 +28,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qv_decode_internal.h"
 
 namespace qv {
@@ -42,6 +44,11 @@ constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 16;     // activation rows of a block (the MFMA's M)
 constexpr int kWindow = 128;  // codes of a window: one 16-byte load by each quarter of a wave
+
+// Variants by size (see the rules' measurements below).
+constexpr int kNarrow = 16 * 256;  // channels that one block of 16 on every CU takes
+constexpr int kFewRows = 4;        // rows up to which lanes read activations directly
+constexpr int kFused1024 = 8, kFused4096 = 3;  // rows up to which every block rotates them by itself
 
 // Rotated rows lie in LDS as floats with 8 floats of padding after every 64, so that the strided reads
 // of the transform's passes and the fragment reads of the four quarters fall in different banks.
@@ -127,16 +134,27 @@ __device__ __forceinline__ bf16x8 widen(unsigned w) {
 __device__ __forceinline__ float gelu(float y) { return 0.5f * y * erfcf(-y * 0.70710678118654752f); }
 
 // Sylvester-order Hadamard transform of one row by K / 8 threads (t of them counted here), times mult / sqrt(K):
-// log2(K) butterfly stages, three in registers per pass over LDS.  Called by every thread of a block.
+// log2(K) butterfly stages, three in registers per pass over LDS.  What a thread reads from memory is loaded
+// ahead; run() is called by every thread of a block.
 template <int K, typename X>
-__device__ __forceinline__ void rotate_row(const X* __restrict__ x, const float* __restrict__ mult, float* row, int t) {
+struct RotateRow {
   static_assert(K == 1024 || K == 4096, "Hadamard width");
-  constexpr float kNorm = K == 1024 ? 0.03125f : 0.015625f;
-  float v[8];
-  auto butterflies = [&](int from) {  // index bits of the register number, from bit `from`
+  static constexpr float kNorm = K == 1024 ? 0.03125f : 0.015625f;
+  static constexpr int kStep = K / 8;
+  Eight<X> e;
+  float f[8];
+
+  __device__ __forceinline__ void load(const X* __restrict__ x, int t) { load_eight(x + 8 * t, e); }
+  __device__ __forceinline__ void load_mult(const float* __restrict__ mult, int t) {
 #pragma unroll
-    for (int h = 1; h < 8; h <<= 1) {
-      if (h < from) continue;
+    for (int j = 0; j < 8; ++j) f[j] = mult ? kNorm * mult[t + j * kStep] : kNorm;
+  }
+
+  // Butterflies over the index bits of the register number, from bit value `from`.
+  template <int from>
+  __device__ __forceinline__ static void butterflies(float (&v)[8]) {
+#pragma unroll
+    for (int h = from; h < 8; h <<= 1) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if ((j & h) == 0) {
@@ -146,10 +164,10 @@ __device__ __forceinline__ void rotate_row(const X* __restrict__ x, const float*
         }
       }
     }
-  };
-  {  // bits 0-2
-    Eight<X> e;
-    load_eight(x + 8 * t, e);
+  }
+
+  __device__ __forceinline__ void run(float* row, int t) const {
+    float v[8];
     if constexpr (sizeof(X) == 2) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -161,32 +179,29 @@ __device__ __forceinline__ void rotate_row(const X* __restrict__ x, const float*
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = e.d[i >> 2][i & 3];
     }
-    butterflies(1);
+    butterflies<1>(v);  // bits 0-2
     f32x4* p = reinterpret_cast<f32x4*>(row + padded(8 * t));
     p[0] = f32x4{v[0], v[1], v[2], v[3]};
     p[1] = f32x4{v[4], v[5], v[6], v[7]};
-  }
-  __syncthreads();
-#pragma unroll
-  for (int bit = 3; bit <= 6; bit += 3) {  // bits 3-5, then 6-8
-    const int low = t & ((1 << bit) - 1), high = t >> bit;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = row[padded(low + (j << bit) + (high << (bit + 3)))];
-    butterflies(1);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) row[padded(low + (j << bit) + (high << (bit + 3)))] = v[j];
     __syncthreads();
-  }
-  constexpr int kStep = K / 8;  // bits 9-11 at K = 4096; at K = 1024 only bit 9, the last of the three
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = row[padded(t + j * kStep)];
-  butterflies(K == 1024 ? 4 : 1);
+    for (int bit = 3; bit <= 6; bit += 3) {  // bits 3-5, then 6-8
+      const int low = t & ((1 << bit) - 1), high = t >> bit;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int k = t + j * kStep;
-    row[padded(k)] = v[j] * (mult ? kNorm * mult[k] : kNorm);
+      for (int j = 0; j < 8; ++j) v[j] = row[padded(low + (j << bit) + (high << (bit + 3)))];
+      butterflies<1>(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) row[padded(low + (j << bit) + (high << (bit + 3)))] = v[j];
+      __syncthreads();
+    }
+    // bits 9-11 at K = 4096; at K = 1024 only bit 9, the last of the three
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = row[padded(t + j * kStep)];
+    butterflies<K == 1024 ? 4 : 1>(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) row[padded(t + j * kStep)] = v[j] * f[j];
   }
-}
+};
 
 template <typename X>
 struct Args {
@@ -197,14 +212,31 @@ struct Args {
   const float* bias;
   void* y;
   int64_t M, ldx, ldy;
-  int N, K, group;
+  int N, K, group, group_shift;  // a window's group: its first code >> group_shift
   int gelu, y_bf16;
 };
 
-// EXACT: fp32 results, codes converted exactly.  KROT: 0: rows are read from memory as they are; else the Hadamard width K, and the block rotates
-// its rows into LDS first.
-template <typename X, int NP, bool EXACT, int NT, int KROT>
+// EXACT: fp32 results, codes converted exactly.  NT: tiles of 16 channels of a block; with fewer of them a
+// wave holds more windows in flight instead, 4 loads of 16 bytes a lane in all.
+// SRC: where a wave's fragments of the rows come from.
+enum Source {
+  kDirect,  // memory: a lane reads its own 32 activations of a window (few rows: few cache lines an instruction)
+  kStaged,  // memory, through an LDS region of the wave's own, so that a row's window is read in one piece
+  kRot1024, kRot4096  // LDS: the block rotates its rows into it first
+};
+template <int SRC>
+constexpr int kWidth = SRC == kRot1024 ? 1024 : (SRC == kRot4096 ? 4096 : 0);
+
+// Rows that a block's rotation writes: at K = 1024 it takes four at a time.
+template <int K>
+__host__ __device__ constexpr int rotated_rows(int rows) {
+  return K == 1024 ? (rows + 3) & ~3 : rows;
+}
+
+template <typename X, int NP, bool EXACT, int NT, int SRC>
 __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
+  constexpr int kDepth = NT == 1 ? 4 : 2;  // windows in flight
+  constexpr int K = kWidth<SRC>;
   extern __shared__ f32x4 lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, c = lane >> 4;
@@ -212,42 +244,84 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   const int64_t m0 = (int64_t)blockIdx.y * kRows;
   const int rows = (int)(a.M - m0 < kRows ? a.M - m0 : kRows);
   const int windows = a.K / kWindow, groups = a.K / a.group;
+  constexpr int kAtOnce = K ? 8 * kThreads / K : 1;  // rows that the block rotates in one go
+  const int part = K ? threadIdx.x / (K / 8) : 0, in_row = K ? threadIdx.x % (K / 8) : 0;
+  RotateRow<K ? K : 1024, X> rotation;
+  auto rotated_row = [&](int m) { return a.x + (m0 + (m + part < rows ? m + part : rows - 1)) * a.ldx; };
+  if constexpr (K != 0) {
+    rotation.load(rotated_row(0), in_row);
+    rotation.load_mult(a.mult, in_row);
+  }
 
-  const uint8_t* wrow[NT];
-  const float* srow[NT];
+  // A wave's windows follow each other, so that both halves of a 128-byte line are asked for together.
+  const int share = (windows + kWaves - 1) / kWaves;
+  const int begin = wave * share, end = begin + share < windows ? begin + share : windows;
+
+  const uint8_t* const wbase = a.wq + (int64_t)n0 * (a.K / 2);
+  const float* const sbase = a.ws + (int64_t)n0 * groups;
+  uint32_t wrow[NT], srow[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    int n = n0 + 16 * t + r;
-    n = n < a.N ? n : a.N - 1;
-    wrow[t] = a.wq + (int64_t)n * (a.K / 2) + 16 * c;
-    srow[t] = a.ws + (int64_t)n * groups;
+    const int n = n0 + 16 * t + r < a.N ? 16 * t + r : a.N - 1 - n0;
+    wrow[t] = (uint32_t)n * (a.K / 2) + 16 * c;
+    srow[t] = (uint32_t)n * groups;
   }
-  u32x4 w[NT];
-  float s[NT];
-  auto load_weights = [&](int win) {
-    const int g = win * kWindow / a.group;
+  u32x4 w[kDepth][NT];
+  auto load_codes = [&](int d, int win) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      w[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[t] + (int64_t)win * (kWindow / 2)));
-      s[t] = srow[t][g];
-    }
+    for (int t = 0; t < NT; ++t)
+      w[d][t] = *reinterpret_cast<const u32x4*>(wbase + wrow[t] + (uint32_t)win * (kWindow / 2));
   };
-  if (wave < windows) load_weights(wave);
+  // Scales of four windows at a time: quarter c of the wave loads those of window first + c.
+  float s[NT];
+  auto load_scales = [&](int first) {
+    const int win = first + c < end ? first + c : end - 1;
+    const uint32_t g = (uint32_t)(win * kWindow) >> a.group_shift;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t] = sbase[srow[t] + g];
+  };
+  if (begin < end) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+      if (begin + d < end) load_codes(d, begin + d);
+    load_scales(begin);
+  }
 
   float* const rot = reinterpret_cast<float*>(lds);
-  constexpr int kRowFloats = KROT ? padded(KROT) : 1;
-  if constexpr (KROT != 0) {
-    constexpr int kAtOnce = 8 * kThreads / KROT;  // rows in one go
-    const int part = threadIdx.x / (KROT / 8), t = threadIdx.x % (KROT / 8);
+  constexpr int kRowFloats = K ? padded(K) : 1;
+  if constexpr (K != 0) {
     for (int m = 0; m < rows; m += kAtOnce) {
-      const int mine = m + part < rows ? m + part : rows - 1;
-      rotate_row<KROT, X>(a.x + (m0 + mine) * a.ldx, a.mult, rot + (m + part) * kRowFloats, t);
+      const RotateRow<K, X> now = rotation;
+      if (m + kAtOnce < rows) rotation.load(rotated_row(m + kAtOnce), in_row);
+      now.run(rot + (m + part) * kRowFloats, in_row);
     }
-    __syncthreads();
   }
   const int row = r < rows ? r : rows - 1;
   const X* const xrow = a.x + (m0 + row) * a.ldx + 32 * c;
   const float* const lrow = rot + row * kRowFloats;
+
+  // Staged rows: a wave reads its window of every row in one piece, 16 bytes a lane, and holds the next
+  // one while it works; 16 bytes of padding a row keep the 16 rows' fragments in different banks.
+  constexpr int kPerLoad = 16 / (int)sizeof(X);                      // activations
+  constexpr int kLanesPerRow = kWindow / kPerLoad;                   // 16 (bf16) or 32 (fp32)
+  constexpr int kLoads = kRows * kLanesPerRow / 64;                  // 4 or 8
+  constexpr int kStageRow = kWindow + kPerLoad;                      // activations
+  X* const stage = reinterpret_cast<X*>(rot) + wave * (kRows * kStageRow);
+  u32x4 xs[SRC == kStaged ? kLoads : 1];
+  auto load_stage = [&](int win) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i * (64 / kLanesPerRow) >= rows) break;
+      const int m = i * (64 / kLanesPerRow) + lane / kLanesPerRow;
+      const int from = m < rows ? m : rows - 1;
+      xs[i] = *reinterpret_cast<const u32x4*>(a.x + (m0 + from) * a.ldx + win * kWindow +
+                                              (lane % kLanesPerRow) * kPerLoad);
+    }
+  };
+  if constexpr (SRC == kStaged) {
+    if (begin < end) load_stage(begin);
+  }
+  if constexpr (K != 0) __syncthreads();
 
   f32x4 y[NT];
 #pragma unroll
@@ -256,49 +330,80 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 
-  for (int win = wave; win < windows; win += kWaves) {
-    u32x4 wc[NT];
-    float sc[NT];
+  // The rows' operands of a window, and the sum of its activations.
+  bf16x8 xf[4][NP];
+  f32x4 sum;
+  auto take_rows = [&](int win) {
+    if constexpr (SRC == kStaged) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) wc[t] = w[t], sc[t] = s[t];
-    f32x4 acc[NT], sum = {0, 0, 0, 0};
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
-    bf16x8 xf[4][NP];
+      for (int i = 0; i < kLoads; ++i) {
+        if (i * (64 / kLanesPerRow) >= rows) break;
+        const int m = i * (64 / kLanesPerRow) + lane / kLanesPerRow;
+        *reinterpret_cast<u32x4*>(stage + m * kStageRow + (lane % kLanesPerRow) * kPerLoad) = xs[i];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (win + 1 < end) load_stage(win + 1);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if constexpr (KROT != 0) {
+      if constexpr (K != 0) {
         Eight<float> e;
         load_eight(lrow + padded(win * kWindow + 32 * c) + 8 * j, e);
         pieces<NP>(e, xf[j]);
       } else {
         Eight<X> e;
-        load_eight(xrow + win * kWindow + 8 * j, e);
+        load_eight(SRC == kStaged ? stage + row * kStageRow + 32 * c + 8 * j : xrow + win * kWindow + 8 * j, e);
         pieces<NP>(e, xf[j]);
       }
     }
-    if (win + kWaves < windows) load_weights(win + kWaves);
+    if constexpr (SRC == kStaged) __builtin_amdgcn_wave_barrier();
+    sum = f32x4{0, 0, 0, 0};
+    if constexpr (!EXACT) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (!EXACT) {
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int p = 0; p < NP; ++p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], ones, sum, 0, 0, 0);
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const bf16x8 wf = EXACT ? widen_exact(wc[t][j]) : widen(wc[t][j]);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], wf, acc[t], 0, 0, 0);
-      }
     }
+  };
+  auto product = [&](const u32x4& codes) {
+    f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int j = 0; j < 4; ++j) {
+      const bf16x8 wf = EXACT ? widen_exact(codes[j]) : widen(codes[j]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[t][i] += EXACT ? 16.0f * sc[t] * acc[t][i] : sc[t] * (acc[t][i] - 24.0f * sum[i]);
+      for (int p = 0; p < NP; ++p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], wf, acc, 0, 0, 0);
+    }
+    return acc;
+  };
+  auto add = [&](f32x4& to, float f, const f32x4& acc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] += EXACT ? 16.0f * f * acc[i] : f * (acc[i] - 24.0f * sum[i]);
+  };
+
+  for (int first = begin; first < end; first += 4) {
+    float sc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sc[t] = s[t];
+    if (first + 4 < end) load_scales(first + 4);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int win = first + d;
+      if (win >= end) break;
+      take_rows(win);
+      f32x4 acc[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t] = product(w[d % kDepth][t]);
+      if (win + kDepth < end) load_codes(d % kDepth, win + kDepth);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) add(y[t], __shfl(sc[t], r + 16 * d), acc[t]);
+    }
   }
 
   // Element (m, n) of tile t at [wave][t][m][n].
-  float* const red = rot + (KROT ? ((rows + 3) & ~3) * kRowFloats : 0);
+  if constexpr (SRC == kStaged) __syncthreads();  // the sums take the staging regions' place
+  float* const red = rot + (K ? rotated_rows<K>(rows) * kRowFloats : 0);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -327,7 +432,10 @@ __global__ __launch_bounds__(K / 8) void rotate_rows_kernel(const X* __restrict_
   __shared__ f32x4 row4[padded(K) / 4];
   float* row = reinterpret_cast<float*>(row4);
   const int t = threadIdx.x;
-  rotate_row<K, X>(x + (int64_t)blockIdx.x * ldx, mult, row, t);
+  RotateRow<K, X> rotation;
+  rotation.load(x + (int64_t)blockIdx.x * ldx, t);
+  rotation.load_mult(mult, t);
+  rotation.run(row, t);
   __syncthreads();
   f32x4* o = reinterpret_cast<f32x4*>(out + (int64_t)blockIdx.x * K + 8 * t);
   const f32x4* p = reinterpret_cast<const f32x4*>(row + padded(8 * t));
@@ -335,12 +443,28 @@ __global__ __launch_bounds__(K / 8) void rotate_rows_kernel(const X* __restrict_
   o[1] = p[1];
 }
 
-template <typename X, int NP, bool EXACT, int NT, int KROT>
+template <typename X, int NP, bool EXACT, int NT, int SRC>
 hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
+  constexpr int K = kWidth<SRC>;
   const unsigned gx = (unsigned)((a.N + 16 * NT - 1) / (16 * NT));
   const int rows = (int)(a.M < kRows ? a.M : kRows);
   size_t bytes = (size_t)kWaves * NT * 256 * 4;
-  if (KROT) bytes += (size_t)((rows + 3) & ~3) * padded(KROT ? KROT : 1) * 4;
+  if (K) bytes += (size_t)rotated_rows<K>(rows) * padded(K) * 4;
+  const size_t staged = (size_t)kWaves * kRows * (kWindow * sizeof(X) + 16);
+  if (SRC == kStaged && bytes < staged) bytes = staged;
+  if (bytes > 65536) {
+    static std::atomic<uint64_t> raised{0};  // a bit for each device whose limit was raised for this kernel
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&w4a16_kernel<X, NP, EXACT, NT, SRC>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      if (e != hipSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
   // grid.y holds 65535 blocks: longer runs go in several launches
   const int64_t step = (int64_t)65535 * kRows;
   for (int64_t m = 0; m < a.M; m += step) {
@@ -348,25 +472,30 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
     b.x += m * a.ldx;
     b.M = a.M - m < step ? a.M - m : step;
     b.y = static_cast<char*>(a.y) + m * a.ldy * (a.y_bf16 ? 2 : 4);
-    w4a16_kernel<X, NP, EXACT, NT, KROT><<<dim3(gx, (unsigned)((b.M + kRows - 1) / kRows)), kThreads, bytes, st>>>(b);
+    w4a16_kernel<X, NP, EXACT, NT, SRC>
+        <<<dim3(gx, (unsigned)((b.M + kRows - 1) / kRows)), kThreads, bytes, st>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <typename X, int NP, bool EXACT, int KROT>
+template <typename X, int NP, bool EXACT, int SRC>
 hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
-  return launch_kernel<X, NP, EXACT, 1, KROT>(a, st);
+  if constexpr (SRC != kDirect) {  // the callers' rule: few rows and few channels
+    if (a.N > 2 * kNarrow) return launch_kernel<X, NP, EXACT, 4, SRC>(a, st);
+    if (a.N > kNarrow) return launch_kernel<X, NP, EXACT, 2, SRC>(a, st);
+  }
+  return launch_kernel<X, NP, EXACT, 1, SRC>(a, st);
 }
 
 // Pieces by the types: rows that are bf16 are one piece; others two or, for fp32 results, three.
-template <typename X, int KROT>
+template <typename X, int SRC>
 hipError_t by_types(const Args<X>& a, hipStream_t st) {
-  if constexpr (sizeof(X) == 2 && KROT == 0)
-    return a.y_bf16 ? by_tiles<X, 1, false, KROT>(a, st) : by_tiles<X, 1, true, KROT>(a, st);
+  if constexpr (sizeof(X) == 2 && kWidth<SRC> == 0)
+    return a.y_bf16 ? by_tiles<X, 1, false, SRC>(a, st) : by_tiles<X, 1, true, SRC>(a, st);
   else
-    return a.y_bf16 ? by_tiles<X, 2, false, KROT>(a, st) : by_tiles<X, 3, true, KROT>(a, st);
+    return a.y_bf16 ? by_tiles<X, 2, false, SRC>(a, st) : by_tiles<X, 3, true, SRC>(a, st);
 }
 
 template <typename X>
@@ -379,14 +508,20 @@ hipError_t rotate_rows(const X* x, int64_t M, int64_t K, int64_t ldx, const floa
 }
 
 template <typename X>
+hipError_t unrotated(const Args<X>& a, hipStream_t st) {
+  return a.M > kFewRows || a.N > kNarrow ? by_types<X, kStaged>(a, st) : by_types<X, kDirect>(a, st);
+}
+
+template <typename X>
 hipError_t launch(Args<X> a, bool rotate, float* rows32, hipStream_t st) {
-  if (!rotate) return by_types<X, 0>(a, st);
-  if (a.K == 1024 && a.M <= 4) return by_types<X, 1024>(a, st);
-  if (a.K == 4096 && a.M == 1) return by_types<X, 4096>(a, st);
+  if (!rotate) return unrotated<X>(a, st);
+  if (a.K == 1024 && a.M <= kFused1024) return by_types<X, kRot1024>(a, st);
+  if (a.K == 4096 && a.M <= kFused4096) return by_types<X, kRot4096>(a, st);
   const hipError_t e = rotate_rows<X>(a.x, a.M, a.K, a.ldx, a.mult, rows32, st);
   if (e != hipSuccess) return e;
-  const Args<float> b = {rows32, nullptr, a.wq, a.ws, a.bias, a.y, a.M, a.K, a.ldy, a.N, a.K, a.group, a.gelu, a.y_bf16};
-  return by_types<float, 0>(b, st);
+  const Args<float> b = {rows32, nullptr, a.wq, a.ws, a.bias, a.y, a.M, a.K, a.ldy, a.N, a.K, a.group,
+                         a.group_shift, a.gelu, a.y_bf16};
+  return unrotated<float>(b, st);
 }
 
 }  // namespace
@@ -394,13 +529,15 @@ hipError_t launch(Args<X> a, bool rotate, float* rows32, hipStream_t st) {
 hipError_t launch_w4a16(const void* X, bool x_bf16, int64_t M, int64_t K, int64_t ldx, bool rotate, const float* mult,
                         const uint8_t* Wq, const float* ws, int64_t group, const float* bias, int64_t N, bool gelu,
                         void* Y, bool y_bf16, int64_t ldy, float* rows32, hipStream_t st) {
+  // group is 128, 256 or 512, or K: one group
+  const int shift = group == K ? 30 : (group == 128 ? 7 : (group == 256 ? 8 : 9));
   if (x_bf16) {
     const Args<__hip_bfloat16> a = {static_cast<const __hip_bfloat16*>(X), mult, Wq, ws, bias, Y, M, ldx, ldy, (int)N,
-                                    (int)K, (int)group, gelu, y_bf16};
+                                    (int)K, (int)group, shift, gelu, y_bf16};
     return launch(a, rotate, rows32, st);
   }
   const Args<float> a = {static_cast<const float*>(X), mult, Wq, ws, bias, Y, M, ldx, ldy, (int)N, (int)K, (int)group,
-                         gelu, y_bf16};
+                         shift, gelu, y_bf16};
   return launch(a, rotate, rows32, st);
 }
 
