@@ -34,8 +34,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kWaves = 4;  // of a block
 constexpr int kTile = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;  // finite, so that differences of maxima are never inf - inf
@@ -127,24 +126,45 @@ struct Values {
       d[0] = __builtin_nontemporal_load(reinterpret_cast<const unsigned*>(p));
     }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) d[i] = 0;
+  }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (INT8) return (float)(int8_t)(d[e >> 2] >> (8 * (e & 3)));
     return (e & 1) ? bits_float(d[e >> 1] & 0xFFFF0000u) : bits_float(d[e >> 1] << 16);
+  }
+  // Channel e of two tokens as a bf16 pair.
+  static __device__ __forceinline__ unsigned pair(const Values& a, const Values& b, int e) {
+    if constexpr (INT8) return __builtin_amdgcn_perm(float_bits(b.get(e)), float_bits(a.get(e)), 0x07060302u);
+    return __builtin_amdgcn_perm(b.d[e >> 1], a.d[e >> 1], (e & 1) ? 0x07060302u : 0x05040100u);
   }
 };
 
 __device__ __forceinline__ void store(float* o, float v) { *o = v; }
 __device__ __forceinline__ void store(__hip_bfloat16* o, float v) { *o = __float2bfloat16(v); }
 
-template <int D, typename X, bool INT8>
-__global__ __launch_bounds__(kThreads) void attention_kernel(Args a) {
+__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {  // of a uniform lane
+  const int lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+
+// W: waves of a block.  ONE: each cache head has one query, which then stands in all 16 columns of the scores, and
+// every lane has the probabilities of its own four tokens: the second product is D / 16 multiply-adds a token on
+// the vector ALU, a quarter of the time that the matrix cores would take for 16 columns.
+template <int D, typename X, bool INT8, bool ONE, int W>
+__global__ __launch_bounds__(64 * W) void attention_kernel(Args a) {
   constexpr int NP = sizeof(X) == 2 ? 1 : 3;  // bf16 pieces of a query
   constexpr int kF = D / 32;                  // operands of the score product
   constexpr int kE = D / 16;
   constexpr int kElem = INT8 ? 1 : 2;
   constexpr int kU = 2;  // tiles at a time
-  __shared__ float red_o[kWaves][kTile][D + 4];
-  __shared__ float red_m[kWaves][kTile], red_l[kWaves][kTile];
+  constexpr int NV = sizeof(X) == 2 ? 2 : 3;  // bf16 pieces of a probability
+  constexpr int kRowsOut = ONE ? 1 : kTile;
+  __shared__ float red_o[W][kRowsOut][D + 4];
+  __shared__ float red_m[W][kRowsOut], red_l[W][kRowsOut];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, c = lane >> 4;
@@ -155,12 +175,31 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(Args a) {
   id /= a.q_tiles;
   const uint32_t h = id % a.heads, b = id / a.heads;
   const uint32_t q0 = q_tile * kTile;
-  const int queries = (int)(a.share - q0 < kTile ? a.share - q0 : kTile);
+  const int queries = ONE ? 1 : (int)(a.share - q0 < kTile ? a.share - q0 : kTile);
 
   const Span sp = span_of(a, b);
-  const int64_t first = sp.first + part * sp.per_part;
-  const int64_t last = first + sp.per_part < sp.last ? first + sp.per_part : sp.last;
+  const int first = (int)(sp.first + part * sp.per_part);
+  const int last = first + sp.per_part < sp.last ? (int)(first + sp.per_part) : (int)sp.last;
   if (first >= last && part > 0) return;
+
+  // Lane i knows where tile i of the wave's next 64 begins: offsets from the cache's start, -1 where there is no page.
+  const uint32_t tiles_per_page = a.page_size / kTile;
+  const int32_t* const table = a.table + (int64_t)b * a.ld_table;
+  const int mine_first = first + wave * kU;
+  const int units = mine_first < last ? (last - mine_first + W * kU - 1) / (W * kU) : 0;
+  int64_t at = -1, scale_at = 0;
+  auto look_up = [&](int unit) {
+    const int tile = mine_first + (unit + lane / kU) * (W * kU) + lane % kU;
+    at = -1;
+    if (tile < last) {
+      const uint32_t entry = (uint32_t)tile / tiles_per_page, slot = ((uint32_t)tile % tiles_per_page) * kTile;
+      const int64_t page = table[entry];
+      if (page >= 0 && page < a.num_pages) {
+        at = page * a.page_stride + h * a.head_stride + (int64_t)slot * a.token_stride;
+        scale_at = (page * a.heads + h) * a.page_size + slot;
+      }
+    }
+  };
 
   const int mine = r < queries ? r : queries - 1;
   bf16x8 q[kF][NP];
@@ -189,46 +228,57 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(Args a) {
     }
   }
 
-  f32x4 o[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = f32x4{0, 0, 0, 0};
-  float m = kLowest, l = 0.0f;  // of query r; l of this lane's tokens
-
-  const uint32_t tiles_per_page = a.page_size / kTile;
-  const int32_t* table = a.table + (int64_t)b * a.ld_table;
   Keys<D, INT8> k[kU];
   Values<D, INT8> v[kU][4];
   f32x4 ks[kU], vs[kU];
-  bool there[kU];
+  // Tokens before `begin` and from `end` on are not read: their lanes read the nearest one inside.
+  auto token = [&](int tile, int t) {
+    const int lo = (int)sp.begin - tile * kTile, hi = (int)sp.end - 1 - tile * kTile;
+    return (uint32_t)(t < lo ? lo : (t > hi ? hi : t)) * (a.token_stride * kElem);
+  };
+  auto load_keys = [&](int u, int tile, int64_t at_u, int64_t scale_u) {
+    k[u].load(a.kp + at_u * kElem, token(tile, r), c);
+    if constexpr (INT8) ks[u] = *reinterpret_cast<const f32x4*>(a.ks + scale_u + 4 * c);
+  };
+  auto load_values = [&](int u, int tile, int64_t at_u, int64_t scale_u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[u][i].load(a.vp + at_u * kElem + token(tile, 4 * c + i) + r * Values<D, INT8>::kBytes);
+    if constexpr (INT8) vs[u] = *reinterpret_cast<const f32x4*>(a.vs + scale_u + 4 * c);
+  };
 
-  for (int64_t tile0 = first + wave * kU; tile0 < last; tile0 += kWaves * kU) {
+  f32x4 o[ONE ? 1 : kE];
+  float o1[ONE ? kE : 1];
+  if constexpr (ONE) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o1[e] = 0.0f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = f32x4{0, 0, 0, 0};
+  }
+  float m = kLowest, l = 0.0f;  // of query r; l of this lane's tokens
+
+  int64_t here[kU], next[kU], scale_next[kU];
+  if (units > 0) {
+    look_up(0);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int64_t tile = tile0 + u;
-      const uint32_t entry = (uint32_t)tile / tiles_per_page, slot = ((uint32_t)tile % tiles_per_page) * kTile;
-      int64_t page = tile < last ? __builtin_amdgcn_readfirstlane(table[entry]) : -1;
-      there[u] = page >= 0 && page < a.num_pages;
-      if (there[u]) {
-        const int64_t at = page * a.page_stride + h * a.head_stride + (int64_t)slot * a.token_stride;
-        // tokens before `begin` and from `end` on are not read: their lanes read the nearest one inside
-        const int lo = (int)(sp.begin - tile * kTile), hi = (int)(sp.end - 1 - tile * kTile);
-        auto inside = [&](int t) { return (uint32_t)(t < lo ? lo : (t > hi ? hi : t)); };
-        k[u].load(a.kp + at * kElem, inside(r) * a.token_stride * kElem, c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[u][i].load(a.vp + at * kElem + inside(4 * c + i) * a.token_stride * kElem + r * Values<D, INT8>::kBytes);
-        if constexpr (INT8) {
-          const int64_t sc = (page * a.heads + h) * a.page_size + slot + 4 * c;
-          ks[u] = *reinterpret_cast<const f32x4*>(a.ks + sc);
-          vs[u] = *reinterpret_cast<const f32x4*>(a.vs + sc);
-        }
+      here[u] = lane_value(at, u);
+      const int64_t sc = INT8 ? lane_value(scale_at, u) : 0;
+      if (here[u] >= 0) {
+        load_keys(u, mine_first + u, here[u], sc);
+        load_values(u, mine_first + u, here[u], sc);
       }
     }
+  }
+  for (int unit = 0; unit < units; ++unit) {
+    const int tile0 = mine_first + unit * (W * kU), tile1 = tile0 + W * kU;
+    const bool more = unit + 1 < units;
     float s[kU][4];
     float top = m;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (!there[u]) {
+      if (here[u] < 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][i] = -INFINITY;
         continue;
@@ -240,58 +290,127 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(Args a) {
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[f][n], acc, 0, 0, 0);
       }
-      const int64_t t0 = (tile0 + u) * kTile + 4 * c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = acc[i] * a.scale;
-        if constexpr (INT8) x *= ks[u][i];
-        s[u][i] = t0 + i >= sp.begin && t0 + i < sp.end ? x : -INFINITY;
-        top = fmaxf(top, s[u][i]);
+      for (int i = 0; i < 4; ++i) s[u][i] = INT8 ? acc[i] * (a.scale * ks[u][i]) : acc[i] * a.scale;
+      const int t0 = (tile0 + u) * kTile;
+      if (t0 < sp.begin || t0 + kTile > sp.end) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s[u][i] = t0 + 4 * c + i >= sp.begin && t0 + 4 * c + i < sp.end ? s[u][i] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[u][i]);
+    }
+    // The next unit's keys are on their way while this one's probabilities and sums are formed.
+    if (more) {
+      if (((unit + 1) * kU) % 64 == 0) look_up(unit + 1);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = ((unit + 1) * kU + u) % 64;
+        next[u] = lane_value(at, i);
+        scale_next[u] = INT8 ? lane_value(scale_at, i) : 0;
+        if (next[u] >= 0) load_keys(u, tile1 + u, next[u], scale_next[u]);
       }
     }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float shrink = exp2f(m - top);
-    m = top;
-    l *= shrink;
+    if (__any(top > m)) {  // otherwise the maxima stand
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float shrink = exp2_raw(m - top);
+      m = top;
+      l *= shrink;
+      if constexpr (ONE) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
+        for (int e = 0; e < kE; ++e) o1[e] *= shrink;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[e][i] *= shrink;
+        for (int e = 0; e < kE; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[e][i] *= shrink;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (!there[u]) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float p = exp2f(s[u][i] - m);
+        float p = exp2_raw(s[u][i] - m);
         l += p;
-        if constexpr (INT8) p = p > 0.0f ? p * vs[u][i] : 0.0f;
+        if constexpr (INT8) p = p > 0.0f ? p * vs[u][i] : 0.0f;  // behind a sequence's end a scale may be anything
+        s[u][i] = p;
+      }
+      if (here[u] < 0) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[u][i].get(e), p, o[e], 0, 0, 0);
+        for (int i = 0; i < 4; ++i) v[u][i].clear();
+      }
+    }
+    if constexpr (ONE) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) o1[e] = fmaf(v[u][i].get(e), s[u][i], o1[e]);
+    } else {
+      bf16x8 p[NV];  // slots 8 c + 4 u + i of the sum: token 4 c + i of tile u
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        u32x4 w;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          float &x = s[z >> 1][2 * (z & 1)], &y = s[z >> 1][2 * (z & 1) + 1];
+          w[z] = __builtin_amdgcn_perm(float_bits(y), float_bits(x), 0x07060302u);
+          x -= bits_float(float_bits(x) & 0xFFFF0000u);
+          y -= bits_float(float_bits(y) & 0xFFFF0000u);
+        }
+        p[n] = __builtin_bit_cast(bf16x8, w);
+      }
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        u32x4 w;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) w[z] = Values<D, INT8>::pair(v[z >> 1][2 * (z & 1)], v[z >> 1][2 * (z & 1) + 1], e);
+        const bf16x8 vf = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+        for (int n = NV - 1; n >= 0; --n) o[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, p[n], o[e], 0, 0, 0);
+      }
+    }
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (next[u] >= 0) load_values(u, tile1 + u, next[u], scale_next[u]);
+        here[u] = next[u];
       }
     }
   }
 
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  if (c == 0) {
+  if (c == 0 && r < kRowsOut) {
     red_m[wave][r] = m;
     red_l[wave][r] = l;
   }
+  if constexpr (ONE) {
 #pragma unroll
-  for (int e = 0; e < kE; ++e)
+    for (int e = 0; e < kE; ++e) {
+      o1[e] += __shfl_xor(o1[e], 16);
+      o1[e] += __shfl_xor(o1[e], 32);
+      if (c == 0) red_o[wave][0][kE * r + e] = o1[e];
+    }
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red_o[wave][r][kE * (4 * c + i) + e] = o[e][i];
+    for (int e = 0; e < kE; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red_o[wave][r][kE * (4 * c + i) + e] = o[e][i];
+  }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < queries * D; idx += kThreads) {
+  for (int idx = threadIdx.x; idx < queries * D; idx += 64 * W) {
     const int j = idx / D, d = idx % D;
     float top = red_m[0][j];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][j]);
+    for (int w = 1; w < W; ++w) top = fmaxf(top, red_m[w][j]);
     float sum = 0.0f, val = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2f(red_m[w][j] - top);
+    for (int w = 0; w < W; ++w) {
+      const float f = exp2_raw(red_m[w][j] - top);
       sum += f * red_l[w][j];
       val += f * red_o[w][j][d];
     }
@@ -299,10 +418,10 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(Args a) {
     if (a.splits == 1) {
       store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, sum > 0.0f ? val / sum : 0.0f);
     } else {
-      const int64_t at = ((int64_t)b * a.q_heads + head) * a.splits + part;
-      a.partial[at * D + d] = val;
+      const int64_t to = ((int64_t)b * a.q_heads + head) * a.splits + part;
+      a.partial[to * D + d] = val;
       if (d == 0) {
-        float* ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * at;
+        float* ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * to;
         ml[0] = top;
         ml[1] = sum;
       }
@@ -310,32 +429,66 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(Args a) {
   }
 }
 
-// Parts joined: one block of D threads to a query head.
+// Parts joined: one block to a query head.  Its threads first weigh the parts, then kJoin / D groups of D threads
+// add every so-many-th part, several loads in flight each.
+constexpr int kJoin = 512;
 template <int D, typename X>
-__global__ __launch_bounds__(D) void join_kernel(Args a) {
+__global__ __launch_bounds__(kJoin) void join_kernel(Args a) {
+  constexpr int kGroups = kJoin / D;
+  __shared__ float weight[kPartsWanted];
+  __shared__ float red[kJoin / 64];
+  __shared__ float sums[kGroups][D];
   const uint32_t b = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
   const Span sp = span_of(a, b);
-  int64_t parts = (sp.last - sp.first + sp.per_part - 1) / sp.per_part;
+  int parts = (int)((sp.last - sp.first + sp.per_part - 1) / sp.per_part);
   if (parts < 1) parts = 1;
   const int64_t at = (int64_t)blockIdx.x * a.splits;
-  const float* ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * at;
-  const float* val = a.partial + at * D + threadIdx.x;
-  float m = kLowest, l = 0.0f, o = 0.0f;
-  for (int64_t p = 0; p < parts; ++p) {
-    const float top = fmaxf(m, ml[2 * p]), f = exp2f(m - top), g = exp2f(ml[2 * p] - top);
-    l = l * f + ml[2 * p + 1] * g;
-    o = o * f + val[p * D] * g;
-    m = top;
+  const float* const ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * at;
+  auto across = [&](float x, auto op) {  // over the block
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x = op(x, __shfl_xor(x, d));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = red[0];
+#pragma unroll
+    for (int w = 1; w < kJoin / 64; ++w) x = op(x, red[w]);
+    return x;
+  };
+  float m = kLowest, l = 0.0f;
+  for (int p = threadIdx.x; p < parts; p += kJoin) m = fmaxf(m, ml[2 * p]);
+  m = across(m, [](float x, float y) { return fmaxf(x, y); });
+  for (int p = threadIdx.x; p < parts; p += kJoin) {
+    weight[p] = exp2_raw(ml[2 * p] - m);
+    l += weight[p] * ml[2 * p + 1];
   }
-  store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + threadIdx.x, l > 0.0f ? o / l : 0.0f);
+  l = across(l, [](float x, float y) { return x + y; });  // and the weights are written
+
+  const int g = threadIdx.x / D, d = threadIdx.x % D;
+  const float* const val = a.partial + at * D + d;
+  float o = 0.0f;
+#pragma unroll 8
+  for (int p = g; p < parts; p += kGroups) o += weight[p] * val[(int64_t)p * D];
+  sums[g][d] = o;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    o = sums[0][d];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) o += sums[i][d];
+    store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, l > 0.0f ? o / l : 0.0f);
+  }
 }
 
 template <int D, typename X, bool INT8>
 hipError_t launch(const Args& a, hipStream_t st) {
-  attention_kernel<D, X, INT8><<<a.B * a.heads * a.q_tiles * a.splits, kThreads, 0, st>>>(a);
+  const unsigned blocks = a.B * a.heads * a.q_tiles * a.splits;
+  if (a.share == 1)
+    attention_kernel<D, X, INT8, true, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
+  else
+    attention_kernel<D, X, INT8, false, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  join_kernel<D, X><<<a.B * a.q_heads, D, 0, st>>>(a);
+  join_kernel<D, X><<<a.B * a.q_heads, kJoin, 0, st>>>(a);
   return hipGetLastError();
 }
 
