@@ -45,34 +45,116 @@ struct Args {
   const char *kp, *vp;
   const float *ks, *vs;
   const int32_t *table, *lens;
-  float* partial;  // [B * q_heads][splits][D], then [B * q_heads][splits][2] (maximum, sum)
+  float* partial;  // [parts][q_heads][D], then [parts][q_heads][2] (maximum, sum)
   int64_t q_ts, q_hs, o_ts, o_hs, page_stride, head_stride, ld_table, num_pages;
-  int64_t capacity, window;
-  uint32_t B, heads, q_heads, share, q_tiles, splits, token_stride, page_size;
+  int64_t few, many;  // parts of all sequences together
+  int32_t few_tiles;   // whether all sequences at their capacity have fewer than 2^31 tiles
+  int32_t capacity, window;  // a window of more than 2^31 - 1 tokens is none
+  uint32_t B, heads, q_heads, share, q_tiles, parts, token_stride, page_size;
   float scale;  // times log2 e
 };
 
 __device__ __forceinline__ float bits_float(unsigned u) { return __builtin_bit_cast(float, u); }
 __device__ __forceinline__ unsigned float_bits(float f) { return __builtin_bit_cast(unsigned, f); }
 
-// Tiles [first, last) of a sequence's attended tokens and the tiles of a part of them.
+// Tokens [begin, end) that a sequence attends to and their tiles [first, last); places are counted in 31 bits.
 struct Span {
-  int64_t begin, end;  // tokens
-  int64_t first, last;
-  int64_t per_part;
+  int begin, end, first, last;
 };
-__device__ __forceinline__ Span span_of(const Args& a, uint32_t b) {
+__device__ __forceinline__ Span span_of(const Args& a, int n) {
   Span s;
-  int64_t n = a.lens[b];
-  n = n < 0 ? 0 : (n > a.capacity ? a.capacity : n);
-  s.end = n;
-  s.begin = a.window > 0 && n > a.window ? n - a.window : 0;
+  s.end = n < 0 ? 0 : (n > a.capacity ? a.capacity : n);
+  s.begin = a.window > 0 && s.end > a.window ? s.end - a.window : 0;
   s.first = s.begin / kTile;
-  s.last = (n + kTile - 1) / kTile;
-  int64_t per = (s.last - s.first + a.splits - 1) / a.splits;
-  const int64_t least = kMinTokensPerPart / kTile;
-  s.per_part = per < least ? least : per;
+  s.last = (s.end + kTile - 1) / kTile;
   return s;
+}
+
+// Sums over the lanes up to each one, by DPP: within rows of 16 lanes, then a row's total to the rows behind it.
+__device__ __forceinline__ int scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
+// Where a part lies.  The tiles of all sequences together give the size of a part; a sequence has as many as that
+// takes, at least one, and the parts of all sequences are numbered through.  A wave's lanes work this
+// out from the lengths, 64 sequences at a time; every result is the same in all lanes.
+struct Part {
+  int b, index;         // sequence and number in it
+  int first_of, count;  // number of the sequence's first part among all, and how many it has
+  int per_part;         // tiles
+  Span span;
+};
+// BY_PART: of part number `which` (b = -1: there is none), else of sequence `which` (index 0).
+template <bool BY_PART>
+__device__ __forceinline__ Part find_part(const Args& a, int which) {
+  const int lane = threadIdx.x & 63, B = (int)a.B;
+  // One round of blocks; more of them where each still has a long part (uneven lengths and starts even out).
+  const int least = (int)kMinTokensPerPart / kTile, enough = (int)kLongPart / kTile;
+  auto size_of_parts = [&](auto total, auto few, auto many) {
+    const int each = (int)((total + few - 1) / few), at_most = (int)((total + many - 1) / many);
+    const int more = at_most > enough ? at_most : enough;
+    const int per = each < more ? each : more;
+    return __builtin_amdgcn_readfirstlane(per < least ? least : per);
+  };
+  Part p;
+  const int mine = lane < B ? a.lens[lane] : 0;  // of the first 64 sequences
+  const Span own = span_of(a, mine);
+  if (B <= 64 && a.few_tiles) {  // the totals fit 32 bits
+    const uint32_t total = __builtin_amdgcn_readlane(scan(own.last - own.first), 63);
+    p.per_part = size_of_parts(total, (uint32_t)a.few, (uint32_t)a.many);
+  } else {
+    uint64_t total = own.last - own.first;
+    for (int i = lane + 64; i < B; i += 64) {
+      const Span s = span_of(a, a.lens[i]);
+      total += s.last - s.first;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+    p.per_part = size_of_parts(total, (uint64_t)a.few, (uint64_t)a.many);
+  }
+  int base = 0;  // parts of the sequences before
+  p.b = -1;
+  for (int first = 0; first < B; first += 64) {
+    const int i = first + lane;
+    const int n = first == 0 ? mine : (i < B ? a.lens[i] : 0);
+    const Span s = span_of(a, n);
+    const int tiles = s.last - s.first;
+    const int count = i < B ? (tiles > p.per_part ? (int)((uint32_t)(tiles + p.per_part - 1) / (uint32_t)p.per_part) : 1) : 0;
+    const int upto = scan(count);
+    const uint64_t hit = BY_PART ? __ballot(i < B && base + upto > which) : __ballot(i == which);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      p.b = first + at;
+      p.count = __builtin_amdgcn_readlane(count, at);
+      p.first_of = base + __builtin_amdgcn_readlane(upto, at) - p.count;
+      p.index = BY_PART ? which - p.first_of : 0;
+      p.span = span_of(a, __builtin_amdgcn_readlane(n, at));
+      break;
+    }
+    base += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return p;
+}
+
+// Byte i of a dword as a signed number, in one instruction.
+template <int i>
+__device__ __forceinline__ float signed_byte(unsigned w) {
+  float f;
+  if constexpr (i == 0)
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(w));
+  else if constexpr (i == 1)
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(w));
+  else if constexpr (i == 2)
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(w));
+  else
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(w));
+  return f;
 }
 
 // Keys of one tile as loaded, and as operands of the score product.
@@ -80,10 +162,10 @@ template <int D, bool INT8>
 struct Keys {
   static constexpr int kLoads = INT8 ? D / 64 : D / 32;
   u32x4 d[kLoads];
-  __device__ __forceinline__ void load(const char* tile, uint32_t token_bytes, int c) {
+  __device__ __forceinline__ void load(const char* tile, uint32_t lane_bytes) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
-      d[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(tile + token_bytes + 64 * j + 16 * c));
+      d[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(tile + lane_bytes + 64 * j));
   }
   // operand f covers channels channel(f, c) .. + 7
   static __device__ __forceinline__ int channel(int f, int c) {
@@ -97,11 +179,8 @@ struct Keys {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const unsigned w = d[f >> 1][2 * (f & 1) + h];
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));  // exact in bf16
-        o[2 * h] = __builtin_amdgcn_perm(float_bits(x[1]), float_bits(x[0]), 0x07060302u);
-        o[2 * h + 1] = __builtin_amdgcn_perm(float_bits(x[3]), float_bits(x[2]), 0x07060302u);
+        o[2 * h] = __builtin_amdgcn_perm(float_bits(signed_byte<1>(w)), float_bits(signed_byte<0>(w)), 0x07060302u);
+        o[2 * h + 1] = __builtin_amdgcn_perm(float_bits(signed_byte<3>(w)), float_bits(signed_byte<2>(w)), 0x07060302u);
       }
       return __builtin_bit_cast(bf16x8, o);
     }
@@ -115,7 +194,8 @@ struct Values {
   static constexpr int kBytes = kE * (INT8 ? 1 : 2);
   static constexpr int kWords = kBytes / 4;
   unsigned d[kWords];
-  __device__ __forceinline__ void load(const char* p) {
+  __device__ __forceinline__ void load(const char* tile, uint32_t lane_bytes) {
+    const char* const p = tile + lane_bytes;
     if constexpr (kWords == 4) {
       const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
       d[0] = v[0], d[1] = v[1], d[2] = v[2], d[3] = v[3];
@@ -131,7 +211,11 @@ struct Values {
     for (int i = 0; i < kWords; ++i) d[i] = 0;
   }
   __device__ __forceinline__ float get(int e) const {
-    if constexpr (INT8) return (float)(int8_t)(d[e >> 2] >> (8 * (e & 3)));
+    if constexpr (INT8) {
+      const unsigned w = d[e >> 2];
+      return (e & 3) == 0 ? signed_byte<0>(w) : (e & 3) == 1 ? signed_byte<1>(w) : (e & 3) == 2 ? signed_byte<2>(w)
+                                                                                                : signed_byte<3>(w);
+    }
     return (e & 1) ? bits_float(d[e >> 1] & 0xFFFF0000u) : bits_float(d[e >> 1] << 16);
   }
   // Channel e of two tokens as a bf16 pair.
@@ -155,7 +239,7 @@ __device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {  // of a un
 // every lane has the probabilities of its own four tokens: the second product is D / 16 multiply-adds a token on
 // the vector ALU, a quarter of the time that the matrix cores would take for 16 columns.
 template <int D, typename X, bool INT8, bool ONE, int W>
-__global__ __launch_bounds__(64 * W) void attention_kernel(Args a) {
+__global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
   constexpr int NP = sizeof(X) == 2 ? 1 : 3;  // bf16 pieces of a query
   constexpr int kF = D / 32;                  // operands of the score product
   constexpr int kE = D / 16;
@@ -166,21 +250,21 @@ __global__ __launch_bounds__(64 * W) void attention_kernel(Args a) {
   __shared__ float red_o[W][kRowsOut][D + 4];
   __shared__ float red_m[W][kRowsOut], red_l[W][kRowsOut];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   uint32_t id = blockIdx.x;
-  const uint32_t part = id % a.splits;
-  id /= a.splits;
   const uint32_t q_tile = id % a.q_tiles;
   id /= a.q_tiles;
-  const uint32_t h = id % a.heads, b = id / a.heads;
+  const uint32_t h = id % a.heads;
+  const uint32_t number = id / a.heads;
+  const Part part = find_part<true>(a, (int)number);
+  if (part.b < 0) return;
+  const uint32_t b = (uint32_t)part.b;
   const uint32_t q0 = q_tile * kTile;
   const int queries = ONE ? 1 : (int)(a.share - q0 < kTile ? a.share - q0 : kTile);
-
-  const Span sp = span_of(a, b);
-  const int first = (int)(sp.first + part * sp.per_part);
-  const int last = first + sp.per_part < sp.last ? (int)(first + sp.per_part) : (int)sp.last;
-  if (first >= last && part > 0) return;
+  const Span sp = part.span;
+  const int first = sp.first + part.index * part.per_part;
+  const int last = first + part.per_part < sp.last ? first + part.per_part : sp.last;
 
   // Lane i knows where tile i of the wave's next 64 begins: offsets from the cache's start, -1 where there is no page.
   const uint32_t tiles_per_page = a.page_size / kTile;
@@ -231,19 +315,30 @@ __global__ __launch_bounds__(64 * W) void attention_kernel(Args a) {
   Keys<D, INT8> k[kU];
   Values<D, INT8> v[kU][4];
   f32x4 ks[kU], vs[kU];
+  const uint32_t token_bytes = a.token_stride * kElem;
+  const uint32_t key_lane = r * token_bytes + 16 * c, value_lane = r * Values<D, INT8>::kBytes;
+  auto edge = [&](int tile) { return tile * kTile < sp.begin || tile * kTile + kTile > sp.end; };
   // Tokens before `begin` and from `end` on are not read: their lanes read the nearest one inside.
-  auto token = [&](int tile, int t) {
-    const int lo = (int)sp.begin - tile * kTile, hi = (int)sp.end - 1 - tile * kTile;
-    return (uint32_t)(t < lo ? lo : (t > hi ? hi : t)) * (a.token_stride * kElem);
+  auto inside = [&](int tile, int t) {
+    const int lo = sp.begin - tile * kTile, hi = sp.end - 1 - tile * kTile;
+    return (uint32_t)(t < lo ? lo : (t > hi ? hi : t));
   };
   auto load_keys = [&](int u, int tile, int64_t at_u, int64_t scale_u) {
-    k[u].load(a.kp + at_u * kElem, token(tile, r), c);
+    uint32_t lane_bytes = key_lane;
+    if (edge(tile)) lane_bytes = inside(tile, r) * token_bytes + 16 * c;
+    k[u].load(a.kp + at_u * kElem, lane_bytes);
     if constexpr (INT8) ks[u] = *reinterpret_cast<const f32x4*>(a.ks + scale_u + 4 * c);
   };
   auto load_values = [&](int u, int tile, int64_t at_u, int64_t scale_u) {
+    uint32_t lane_bytes[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[u][i].load(a.vp + at_u * kElem + token(tile, 4 * c + i) + r * Values<D, INT8>::kBytes);
+    for (int i = 0; i < 4; ++i) lane_bytes[i] = (4 * c + i) * token_bytes + value_lane;
+    if (edge(tile)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lane_bytes[i] = inside(tile, 4 * c + i) * token_bytes + value_lane;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[u][i].load(a.vp + at_u * kElem, lane_bytes[i]);
     if constexpr (INT8) vs[u] = *reinterpret_cast<const f32x4*>(a.vs + scale_u + 4 * c);
   };
 
@@ -293,7 +388,7 @@ __global__ __launch_bounds__(64 * W) void attention_kernel(Args a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[u][i] = INT8 ? acc[i] * (a.scale * ks[u][i]) : acc[i] * a.scale;
       const int t0 = (tile0 + u) * kTile;
-      if (t0 < sp.begin || t0 + kTile > sp.end) {
+      if (edge(tile0 + u)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           s[u][i] = t0 + 4 * c + i >= sp.begin && t0 + 4 * c + i < sp.end ? s[u][i] : -INFINITY;
@@ -415,13 +510,13 @@ __global__ __launch_bounds__(64 * W) void attention_kernel(Args a) {
       val += f * red_o[w][j][d];
     }
     const uint32_t head = h * a.share + q0 + j;
-    if (a.splits == 1) {
+    if (part.count == 1) {
       store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, sum > 0.0f ? val / sum : 0.0f);
     } else {
-      const int64_t to = ((int64_t)b * a.q_heads + head) * a.splits + part;
+      const int64_t to = (int64_t)number * a.q_heads + head;
       a.partial[to * D + d] = val;
       if (d == 0) {
-        float* ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * to;
+        float* ml = a.partial + (int64_t)a.parts * a.q_heads * D + 2 * to;
         ml[0] = top;
         ml[1] = sum;
       }
@@ -435,15 +530,16 @@ constexpr int kJoin = 512;
 template <int D, typename X>
 __global__ __launch_bounds__(kJoin) void join_kernel(Args a) {
   constexpr int kGroups = kJoin / D;
-  __shared__ float weight[kPartsWanted];
+  __shared__ float weight[kManyBlocks + 1];
   __shared__ float red[kJoin / 64];
   __shared__ float sums[kGroups][D];
   const uint32_t b = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
-  const Span sp = span_of(a, b);
-  int parts = (int)((sp.last - sp.first + sp.per_part - 1) / sp.per_part);
-  if (parts < 1) parts = 1;
-  const int64_t at = (int64_t)blockIdx.x * a.splits;
-  const float* const ml = a.partial + (int64_t)a.B * a.q_heads * a.splits * D + 2 * at;
+  const Part part = find_part<false>(a, (int)b);
+  const int parts = part.count;
+  if (parts == 1) return;  // its one block has written the result
+  const int64_t at = (int64_t)part.first_of * a.q_heads + head;
+  const int64_t step = a.q_heads;
+  const float* const ml = a.partial + (int64_t)a.parts * a.q_heads * D + 2 * at;
   auto across = [&](float x, auto op) {  // over the block
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) x = op(x, __shfl_xor(x, d));
@@ -456,11 +552,11 @@ __global__ __launch_bounds__(kJoin) void join_kernel(Args a) {
     return x;
   };
   float m = kLowest, l = 0.0f;
-  for (int p = threadIdx.x; p < parts; p += kJoin) m = fmaxf(m, ml[2 * p]);
+  for (int p = threadIdx.x; p < parts; p += kJoin) m = fmaxf(m, ml[2 * p * step]);
   m = across(m, [](float x, float y) { return fmaxf(x, y); });
   for (int p = threadIdx.x; p < parts; p += kJoin) {
-    weight[p] = exp2_raw(ml[2 * p] - m);
-    l += weight[p] * ml[2 * p + 1];
+    weight[p] = exp2_raw(ml[2 * p * step] - m);
+    l += weight[p] * ml[2 * p * step + 1];
   }
   l = across(l, [](float x, float y) { return x + y; });  // and the weights are written
 
@@ -468,7 +564,7 @@ __global__ __launch_bounds__(kJoin) void join_kernel(Args a) {
   const float* const val = a.partial + at * D + d;
   float o = 0.0f;
 #pragma unroll 8
-  for (int p = g; p < parts; p += kGroups) o += weight[p] * val[(int64_t)p * D];
+  for (int p = g; p < parts; p += kGroups) o += weight[p] * val[p * step * D];
   sums[g][d] = o;
   __syncthreads();
   if (threadIdx.x < D) {
@@ -480,14 +576,14 @@ __global__ __launch_bounds__(kJoin) void join_kernel(Args a) {
 }
 
 template <int D, typename X, bool INT8>
-hipError_t launch(const Args& a, hipStream_t st) {
-  const unsigned blocks = a.B * a.heads * a.q_tiles * a.splits;
+hipError_t launch(const Args& a, bool split, hipStream_t st) {
+  const unsigned blocks = a.parts * a.heads * a.q_tiles;
   if (a.share == 1)
     attention_kernel<D, X, INT8, true, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
   else
     attention_kernel<D, X, INT8, false, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
+  if (e != hipSuccess || !split) return e;
   join_kernel<D, X><<<a.B * a.q_heads, kJoin, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -514,24 +610,28 @@ hipError_t launch_paged_attention(const AttentionArgs& in, hipStream_t st) {
   a.head_stride = c.head_stride;
   a.ld_table = in.ld_table;
   a.num_pages = c.num_pages;
-  a.capacity = in.max_pages * c.page_size;
-  a.window = in.window;
+  a.capacity = (int32_t)(in.max_pages * c.page_size);
+  a.window = in.window > 0x7fffffff ? 0 : (int32_t)in.window;
   a.B = (uint32_t)in.B;
   a.heads = (uint32_t)c.heads;
   a.q_heads = (uint32_t)in.q_heads;
   a.share = (uint32_t)(in.q_heads / c.heads);
   a.q_tiles = (a.share + kTile - 1) / kTile;
-  a.splits = (uint32_t)paged_attention_splits(in.B, in.q_heads, c.heads, a.capacity);
+  const AttentionParts parts = paged_attention_parts(in.B, in.q_heads, c.heads, a.capacity);
+  a.few = parts.few;
+  a.many = parts.many;
+  a.few_tiles = (in.max_pages * c.page_size + kTile) / kTile * in.B < (int64_t{1} << 31) - kManyBlocks;
+  a.parts = (uint32_t)parts.most;
   a.token_stride = (uint32_t)c.token_stride;
   a.page_size = (uint32_t)c.page_size;
   a.scale = in.scale * kLog2e;
   const bool q8 = c.dtype == QV_KV_INT8;
   if (c.head_dim == 64) {
-    if (in.bf16) return q8 ? launch<64, __hip_bfloat16, true>(a, st) : launch<64, __hip_bfloat16, false>(a, st);
-    return q8 ? launch<64, float, true>(a, st) : launch<64, float, false>(a, st);
+    if (in.bf16) return q8 ? launch<64, __hip_bfloat16, true>(a, parts.split, st) : launch<64, __hip_bfloat16, false>(a, parts.split, st);
+    return q8 ? launch<64, float, true>(a, parts.split, st) : launch<64, float, false>(a, parts.split, st);
   }
-  if (in.bf16) return q8 ? launch<128, __hip_bfloat16, true>(a, st) : launch<128, __hip_bfloat16, false>(a, st);
-  return q8 ? launch<128, float, true>(a, st) : launch<128, float, false>(a, st);
+  if (in.bf16) return q8 ? launch<128, __hip_bfloat16, true>(a, parts.split, st) : launch<128, __hip_bfloat16, false>(a, parts.split, st);
+  return q8 ? launch<128, float, true>(a, parts.split, st) : launch<128, float, false>(a, parts.split, st);
 }
 
 }  // namespace qv

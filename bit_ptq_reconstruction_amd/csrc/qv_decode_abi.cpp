@@ -187,9 +187,9 @@ size_t qv_paged_attention_workspace_size(int64_t B, int64_t q_heads, int64_t hea
   if (B < 0 || heads <= 0 || heads > 65536 || q_heads <= 0 || q_heads > 65536 || q_heads % heads != 0 ||
       (head_dim != 64 && head_dim != 128) || capacity < 0 || capacity > kMaxInt || B > kMaxInt / q_heads)
     return 0;
-  const int64_t splits = qv::paged_attention_splits(B, q_heads, heads, capacity);
-  if (splits == 1) return 256;
-  return round256(static_cast<size_t>(B * q_heads * splits) * static_cast<size_t>(head_dim + 2) * 4 + 1);
+  const qv::AttentionParts p = qv::paged_attention_parts(B, q_heads, heads, capacity);
+  if (!p.split) return 256;
+  return round256(static_cast<size_t>(p.most * q_heads) * static_cast<size_t>(head_dim + 2) * 4 + 1);
 }
 
 qv_status qv_paged_attention(const qv_heads* Q, qv_dtype q_dtype, int64_t B, int64_t q_heads, const qv_kv_cache* cache,

@@ -41,22 +41,30 @@ struct AttentionArgs {
   const int32_t* lens;
   float scale;
   int64_t window;
-  float* partial;  // scratch of paged_attention_splits() > 1
+  float* partial;  // scratch for the parts of split sequences
 };
 hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t st);
 
-// Parts that the length is split into at most: enough for the partial results to fill the chip.
-// Each part keeps head_dim + 2 floats for every query head.
-constexpr int64_t kQueriesPerBlock = 16;   // query heads of one cache head that a block takes
-constexpr int64_t kMinTokensPerPart = 256;  // a shorter part costs more in the join than it saves
-constexpr int64_t kPartsWanted = 2048;      // 256 CUs x 8 blocks
-inline int64_t paged_attention_splits(int64_t B, int64_t q_heads, int64_t heads, int64_t capacity) {
-  const int64_t tiles = (q_heads / heads + kQueriesPerBlock - 1) / kQueriesPerBlock;
-  const int64_t blocks = B * heads * tiles;
-  int64_t n = blocks > 0 ? (kPartsWanted + blocks - 1) / blocks : 1;
-  const int64_t most = (capacity + kMinTokensPerPart - 1) / kMinTokensPerPart;
-  if (n > most) n = most;
-  return n < 1 ? 1 : n;
+// How the batch's tokens are cut into parts of equal size.  `few` parts of all sequences together are one round of
+// blocks on the chip, `many` five; each sequence adds at most one part that is not full, and none has more
+// than its capacity holds.  Each part keeps head_dim + 2 floats for every query head.
+constexpr int64_t kQueriesPerBlock = 16;    // query heads of one cache head that a block takes
+constexpr int64_t kMinTokensPerPart = 128;  // a unit of work for each wave of a block
+constexpr int64_t kLongPart = 1536;         // tokens from which a block's start no longer counts
+constexpr int64_t kFewBlocks = 768, kManyBlocks = 4096;
+struct AttentionParts {
+  int64_t few, many, most;
+  bool split;  // whether a sequence can have more than one
+};
+inline AttentionParts paged_attention_parts(int64_t B, int64_t q_heads, int64_t heads, int64_t capacity) {
+  const int64_t each = heads * ((q_heads / heads + kQueriesPerBlock - 1) / kQueriesPerBlock);  // blocks of a part
+  AttentionParts p;
+  p.few = (kFewBlocks + each - 1) / each;
+  p.many = (kManyBlocks + each - 1) / each;
+  p.split = capacity > kMinTokensPerPart;
+  const int64_t full = (capacity + kMinTokensPerPart - 1) / kMinTokensPerPart;
+  p.most = !p.split ? B : (B * full < p.many + B ? B * full : p.many + B);
+  return p;
 }
 
 }  // namespace qv
