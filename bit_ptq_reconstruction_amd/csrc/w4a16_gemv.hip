@@ -48,7 +48,7 @@ constexpr int kWindow = 128;  // codes of a window: one 16-byte load by each qua
 // Variants by size (see the rules' measurements below).
 constexpr int kNarrow = 16 * 256;  // channels that one block of 16 on every CU takes
 constexpr int kFewRows = 4;        // rows up to which lanes read activations directly
-constexpr int kFused1024 = 8, kFused4096 = 3;  // rows up to which every block rotates them by itself
+constexpr int kFused1024 = 12, kFused4096 = 4;  // rows up to which every block rotates them by itself
 
 // Rotated rows lie in LDS as floats with 8 floats of padding after every 64, so that the strided reads
 // of the transform's passes and the fragment reads of the four quarters fall in different banks.
@@ -133,18 +133,19 @@ __device__ __forceinline__ bf16x8 widen(unsigned w) {
 
 __device__ __forceinline__ float gelu(float y) { return 0.5f * y * erfcf(-y * 0.70710678118654752f); }
 
-// Sylvester-order Hadamard transform of one row by K / 8 threads (t of them counted here), times mult / sqrt(K):
-// log2(K) butterfly stages, three in registers per pass over LDS.  What a thread reads from memory is loaded
-// ahead; run() is called by every thread of a block.
-template <int K, typename X>
-struct RotateRow {
+// Sylvester-order Hadamard transform of up to B rows, each by K / 8 threads (t of them counted here), times
+// mult / sqrt(K): log2(K) butterfly stages, three in registers per pass over LDS.  The rows go through the passes
+// together, so that they share the barriers.  What a thread reads from memory is loaded ahead; run() is called
+// by every thread of a block.
+template <int K, typename X, int B>
+struct RotateRows {
   static_assert(K == 1024 || K == 4096, "Hadamard width");
   static constexpr float kNorm = K == 1024 ? 0.03125f : 0.015625f;
   static constexpr int kStep = K / 8;
-  Eight<X> e;
+  Eight<X> e[B];
   float f[8];
 
-  __device__ __forceinline__ void load(const X* __restrict__ x, int t) { load_eight(x + 8 * t, e); }
+  __device__ __forceinline__ void load(int b, const X* __restrict__ x, int t) { load_eight(x + 8 * t, e[b]); }
   __device__ __forceinline__ void load_mult(const float* __restrict__ mult, int t) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = mult ? kNorm * mult[t + j * kStep] : kNorm;
@@ -166,40 +167,59 @@ struct RotateRow {
     }
   }
 
-  __device__ __forceinline__ void run(float* row, int t) const {
-    float v[8];
-    if constexpr (sizeof(X) == 2) {
+  // Row b's result at row + b * stride; rows from `count` on are left out (the same in every thread).
+  __device__ __forceinline__ void run(float* row, int stride, int count, int t) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const unsigned w = e.d[i];
-        v[2 * i] = bits_float(w << 16);
-        v[2 * i + 1] = bits_float(w & 0xFFFF0000u);
+    for (int b = 0; b < B; ++b) {
+      if (b >= count) break;
+      float v[8];
+      if constexpr (sizeof(X) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned w = e[b].d[i];
+          v[2 * i] = bits_float(w << 16);
+          v[2 * i + 1] = bits_float(w & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = e[b].d[i >> 2][i & 3];
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = e.d[i >> 2][i & 3];
+      butterflies<1>(v);  // bits 0-2
+      f32x4* p = reinterpret_cast<f32x4*>(row + b * stride + padded(8 * t));
+      p[0] = f32x4{v[0], v[1], v[2], v[3]};
+      p[1] = f32x4{v[4], v[5], v[6], v[7]};
     }
-    butterflies<1>(v);  // bits 0-2
-    f32x4* p = reinterpret_cast<f32x4*>(row + padded(8 * t));
-    p[0] = f32x4{v[0], v[1], v[2], v[3]};
-    p[1] = f32x4{v[4], v[5], v[6], v[7]};
     __syncthreads();
 #pragma unroll
-    for (int bit = 3; bit <= 6; bit += 3) {  // bits 3-5, then 6-8
-      const int low = t & ((1 << bit) - 1), high = t >> bit;
+    for (int bit = 3; bit <= 6; bit += 3) {  // bits 3-5, then 6-8: elements a fixed step apart, padding included
+      const int first = padded((t & ((1 << bit) - 1)) + ((t >> bit) << (bit + 3)));
+      constexpr int kSteps[2] = {8, padded(64)};
+      const int step = kSteps[bit / 3 - 1];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = row[padded(low + (j << bit) + (high << (bit + 3)))];
-      butterflies<1>(v);
+      for (int b = 0; b < B; ++b) {
+        if (b >= count) break;
+        float* const x = row + b * stride + first;
+        float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) row[padded(low + (j << bit) + (high << (bit + 3)))] = v[j];
+        for (int j = 0; j < 8; ++j) v[j] = x[j * step];
+        butterflies<1>(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j * step] = v[j];
+      }
       __syncthreads();
     }
     // bits 9-11 at K = 4096; at K = 1024 only bit 9, the last of the three
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = row[padded(t + j * kStep)];
-    butterflies<K == 1024 ? 4 : 1>(v);
+    for (int b = 0; b < B; ++b) {
+      if (b >= count) break;
+      float* const x = row + b * stride + padded(t);
+      float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) row[padded(t + j * kStep)] = v[j] * f[j];
+      for (int j = 0; j < 8; ++j) v[j] = x[j * padded(kStep)];
+      butterflies<K == 1024 ? 4 : 1>(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j * padded(kStep)] = v[j] * f[j];
+    }
   }
 };
 
@@ -244,12 +264,16 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   const int64_t m0 = (int64_t)blockIdx.y * kRows;
   const int rows = (int)(a.M - m0 < kRows ? a.M - m0 : kRows);
   const int windows = a.K / kWindow, groups = a.K / a.group;
-  constexpr int kAtOnce = K ? 8 * kThreads / K : 1;  // rows that the block rotates in one go
+  // Rotation: `kAtOnce` rows side by side, as often as there are rows.
+  constexpr int kAtOnce = K ? 8 * kThreads / K : 1, kBatch = kAtOnce == 1 ? kFused4096 : (kFused1024 + 3) / 4;
   const int part = K ? threadIdx.x / (K / 8) : 0, in_row = K ? threadIdx.x % (K / 8) : 0;
-  RotateRow<K ? K : 1024, X> rotation;
-  auto rotated_row = [&](int m) { return a.x + (m0 + (m + part < rows ? m + part : rows - 1)) * a.ldx; };
+  RotateRows<K ? K : 1024, X, kBatch> rotation;
   if constexpr (K != 0) {
-    rotation.load(rotated_row(0), in_row);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int m = i * kAtOnce + part;
+      if (i * kAtOnce < rows) rotation.load(i, a.x + (m0 + (m < rows ? m : rows - 1)) * a.ldx, in_row);
+    }
     rotation.load_mult(a.mult, in_row);
   }
 
@@ -289,13 +313,8 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
 
   float* const rot = reinterpret_cast<float*>(lds);
   constexpr int kRowFloats = K ? padded(K) : 1;
-  if constexpr (K != 0) {
-    for (int m = 0; m < rows; m += kAtOnce) {
-      const RotateRow<K, X> now = rotation;
-      if (m + kAtOnce < rows) rotation.load(rotated_row(m + kAtOnce), in_row);
-      now.run(rot + (m + part) * kRowFloats, in_row);
-    }
-  }
+  if constexpr (K != 0)
+    rotation.run(rot + part * kRowFloats, kAtOnce * kRowFloats, (rows + kAtOnce - 1) / kAtOnce, in_row);
   const int row = r < rows ? r : rows - 1;
   const X* const xrow = a.x + (m0 + row) * a.ldx + 32 * c;
   const float* const lrow = rot + row * kRowFloats;
@@ -432,10 +451,10 @@ __global__ __launch_bounds__(K / 8) void rotate_rows_kernel(const X* __restrict_
   __shared__ f32x4 row4[padded(K) / 4];
   float* row = reinterpret_cast<float*>(row4);
   const int t = threadIdx.x;
-  RotateRow<K, X> rotation;
-  rotation.load(x + (int64_t)blockIdx.x * ldx, t);
+  RotateRows<K, X, 1> rotation;
+  rotation.load(0, x + (int64_t)blockIdx.x * ldx, t);
   rotation.load_mult(mult, t);
-  rotation.run(row, t);
+  rotation.run(row, 0, 1, t);
   __syncthreads();
   f32x4* o = reinterpret_cast<f32x4*>(out + (int64_t)blockIdx.x * K + 8 * t);
   const f32x4* p = reinterpret_cast<const f32x4*>(row + padded(8 * t));
