@@ -143,6 +143,12 @@ int64_t whole(PyObject* o) {
   return v;
 }
 
+// Any other number stands for one that the library refuses.
+qv_epilogue epilogue(PyObject* o) {
+  const int64_t v = whole(o);
+  return v == QV_EPI_NONE ? QV_EPI_NONE : (v == QV_EPI_GELU ? QV_EPI_GELU : (qv_epilogue)-1);
+}
+
 void* address(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
 PyObject* qv_error = nullptr;  // the package's QVError
@@ -223,7 +229,7 @@ void linear_device(Call& c, const Linear& l) {
 PyObject* w4a16_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("qv_w4a16_gemv", n, 8, [&](Call& c) {
     const Linear l = linear_operands(c, a[0], a[1], a[2], a[3], a[4], a[5]);
-    const qv_epilogue epi = (qv_epilogue)whole(a[6]);
+    const qv_epilogue epi = epilogue(a[6]);
     linear_device(c, l);
     const c10::hip::HIPGuard on((c10::DeviceIndex)c.device);
     return done(c, qv_w4a16_gemv(l.X->data_ptr(), l.xt, l.M, l.K, l.ldx, (const uint8_t*)l.Wq->data_ptr(),
@@ -240,7 +246,7 @@ PyObject* w4a16_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (inv) c.dense("inv_smooth", *inv, at::kFloat, {l.K});
     const at::Tensor& work = c.tensor("workspace", a[7]);
     void* w = c.workspace(work, qv_w4a16_linear_workspace_size(l.M, l.K));
-    const qv_epilogue epi = (qv_epilogue)whole(a[8]);
+    const qv_epilogue epi = epilogue(a[8]);
     linear_device(c, l);
     if (inv) c.on_gpu(*inv);
     c.on_gpu(work);

@@ -1,0 +1,101 @@
+"""One transformer block that takes its tokens as they come: a frame's tokens at once, then one new token of every
+sequence at a time, with 4-bit weights throughout and the keys and values of the past in a paged cache.
+
+A frame runs through the W4A4 linears (tiles of 128 rows, activations rounded to 4 bits), single tokens through the
+few-row linears (activations not rounded), both over the same packed weights with group scales.  Keys and queries
+are turned by the tokens' positions on an image grid (row and column) or in a line.
+
+    y = x + proj(attention(qkv(norm(x)))),   out = y + fc2(gelu(fc1(norm(y))))
+"""
+from __future__ import annotations
+
+from . import configs
+
+GROUP = 128
+
+
+class StreamBlock:
+    """``weights``: {"qkv", "proj", "fc1", "fc2"} -> [N, K] fp32/bf16 of a block of width 1024 with ``heads`` heads.
+
+    Buffers for ``sequences`` sequences of up to ``capacity`` tokens are allocated here and nothing later, so a step
+    can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle."""
+
+    def __init__(self, qv, weights, sequences: int, capacity: int, device, heads: int = 16, axes: int = 1,
+                 positions: int = 4096, base: float = 10000.0, int8_cache: bool = False, page_size: int = 64,
+                 frame_tokens: int = 0):
+        import torch
+
+        self.qv, self.B, self.heads, self.width = qv, sequences, heads, 1024
+        self.dim = self.width // heads
+        empty = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=device)
+        byte = lambda n: empty(n, dtype=torch.uint8)
+        self.linears = {lin.name: lin for lin in configs.block_linears()}
+        self.Wq, self.ws = {}, {}
+        for name, lin in self.linears.items():
+            self.Wq[name] = empty(lin.N, lin.K // 2, dtype=torch.uint8)
+            self.ws[name] = empty(lin.N, lin.K // GROUP, dtype=torch.float32)
+            qv.qv_pack_weights_grouped(weights[name].contiguous(), None, GROUP, self.Wq[name], self.ws[name])
+        pages = -(-capacity // page_size)
+        shape = (sequences * pages, heads, page_size, self.dim)
+        kind = torch.int8 if int8_cache else torch.bfloat16
+        scales = [torch.zeros(shape[:3], device=device) for _ in range(2)] if int8_cache else [None, None]
+        self.cache = qv.QVKVCache(torch.zeros(shape, dtype=kind, device=device),
+                                  torch.zeros(shape, dtype=kind, device=device), *scales)
+        self.table = torch.arange(sequences * pages, dtype=torch.int32, device=device).view(sequences, pages)
+        self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
+        self.position = torch.zeros((sequences, axes), dtype=torch.int32, device=device)
+        w = self.dim // axes
+        angle = torch.arange(positions, device=device)[:, None] * base ** (-torch.arange(0, w, 2, device=device) / w)
+        self.cos, self.sin = angle.cos(), angle.sin()
+        self.one = self._buffers(sequences, empty, byte, few=True)
+        self.frame = self._buffers(frame_tokens, empty, byte, few=False) if frame_tokens else None
+
+    def _buffers(self, rows, empty, byte, few: bool):
+        qv = self.qv
+        b = {name: empty(rows, lin.N) for name, lin in self.linears.items()}
+        b["q"], b["o"] = empty(rows, self.heads, self.dim), empty(rows, self.heads, self.dim)
+        size = qv.qv_w4a16_linear_workspace_size if few else lambda M, K: qv.qv_w4a4_linear_grouped_workspace_size(M, K, GROUP)
+        b["work"] = byte(max(size(rows, lin.K) for lin in self.linears.values()))
+        if few:
+            b["parts"] = byte(qv.qv_paged_attention_workspace_size(rows, self.heads, self.heads, self.dim,
+                                                                   self.table.shape[1] * self.cache.page_size))
+        return b
+
+    def _linear(self, name, x, b, few: bool):
+        lin, qv = self.linears[name], self.qv
+        if few:
+            qv.qv_w4a16_linear(x, None, self.Wq[name], self.ws[name], GROUP, None, b[name], b["work"], lin.epi)
+        else:
+            qv.qv_w4a4_linear_grouped(x, None, GROUP, self.Wq[name], self.ws[name], None, b[name], b["work"], lin.epi)
+        return b[name]
+
+    def _norm(self, x):
+        import torch
+
+        return torch.nn.functional.layer_norm(x, (self.width,))
+
+    def _heads(self, qkv):
+        qkv = qkv.view(-1, 3, self.heads, self.dim)
+        return qkv[:, 0], qkv[:, 1], qkv[:, 2]
+
+    def take_frame(self, x, sequence: int, position) -> None:
+        """Keys and values of a frame's tokens x [T, 1024] join ``sequence`` (position [T, axes] int32).  Attention
+        inside a frame is not part of this class."""
+        import torch
+
+        T, b = x.shape[0], self.frame
+        q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=False))
+        index = self.lens[sequence] + torch.arange(T, dtype=torch.int32, device=x.device)
+        owner = torch.full_like(index, sequence)
+        self.qv.qv_kv_append(self.cache, self.table, owner, index, k, v, self.cos, self.sin, position)
+        self.lens[sequence] += T
+
+    def step(self, x):
+        """One new token x [B, 1024] bf16 of every sequence, at ``self.position`` [B, axes]; returns the block's output."""
+        qv, b = self.qv, self.one
+        q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=True))
+        qv.qv_kv_append(self.cache, self.table, None, self.lens, k, v, self.cos, self.sin, self.position, q, b["q"])
+        self.lens += 1
+        qv.qv_paged_attention(b["q"], self.cache, self.table, self.lens, b["o"], b["parts"])
+        y = x + self._linear("proj", b["o"].view(self.B, self.width), b, few=True)
+        return y + self._linear("fc2", self._linear("fc1", self._norm(y), b, few=True), b, few=True)

@@ -622,3 +622,113 @@ def test_results_repeat(qv, dev):
     Q = torch.randn((2, 8, 128), generator=g).to(dev)
     a, b = (attend(qv, dev, Q, cache, table.to(dev), lens).clone() for _ in range(2))
     assert torch.equal(a, b)
+
+
+# -------------------------------------------------------------------- many sequences, long parts, a block
+
+def test_attention_many_sequences(qv, dev):
+    """More sequences than a wave has lanes, empty ones among them, and lengths that are cut into parts."""
+    g = gen(9)
+    lens = torch.randint(0, 40, (150,), generator=g).tolist()
+    lens[0], lens[63], lens[64], lens[100], lens[149] = 0, 1500, 700, 3000, 0
+    table, pages = shuffled_table(lens, 16, g)
+    cache = make_cache(qv, dev, pages, 2, 16, 64, "bf16", 0)
+    kv = fill(cache, table, lens, g)
+    for share in (1, 3):
+        Q = torch.randn((150, 2 * share, 64), generator=g)
+        O = attend(qv, dev, Q.to(dev), cache, table.to(dev), lens)
+        o, mag = attention64(Q, kv, lens, 0, 0.125)
+        check_attention(O, o, mag, "fp32", f"150 sequences, share {share}")
+        assert bool((O[[n == 0 for n in lens]] == 0).all())
+
+
+def test_attention_vast_table(qv, dev):
+    """A page table whose capacity over all sequences passes 2^31 tiles of 16 tokens."""
+    g = gen(10)
+    size, B = 65536, 17
+    pages = 2
+    cache = make_cache(qv, dev, pages, 1, size, 64, "bf16", 0)
+    table = torch.full((B, 32767), -1, dtype=torch.int32)
+    lens = [0] * B
+    table[3, 0], table[11, 0], lens[3], lens[11] = 1, 0, 900, 33
+    kv = fill(cache, table, lens, g)
+    Q = torch.randn((B, 2, 64), generator=g)
+    O = attend(qv, dev, Q.to(dev), cache, table.to(dev), lens)
+    o, mag = attention64(Q, kv, lens, 0, 0.125)
+    check_attention(O, o, mag, "fp32", "vast table")
+
+
+@pytest.mark.parametrize("heads,share,kind", [(64, 1, "bf16"), (32, 2, "int8")])
+def test_attention_repeated_pages(qv, dev, heads, share, kind):
+    """393216 tokens on three pages in turn: every token counts equally often, so the result is that of 48 tokens.  A wave
+    takes more than 64 tiles."""
+    g = gen(12)
+    cache = make_cache(qv, dev, 3, heads, 16, 64, kind, 0)
+    kv = fill(cache, torch.arange(3, dtype=torch.int32)[None], [48], g)
+    table = torch.arange(3, dtype=torch.int32).repeat(8192)[None].contiguous()
+    Q = torch.randn((1, heads * share, 64), generator=g)
+    O = attend(qv, dev, Q.to(dev), cache, table.to(dev), [48 * 8192])
+    o, mag = attention64(Q, kv, [48], 0, 0.125)
+    check_attention(O, o, mag, "fp32", "repeated pages")
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_stream_block(qv, dev, int8):
+    """A frame, then single tokens: the block's output against the same block computed plainly in 64 bits from the packed
+    weights.  Roundings to bf16 on the way (norm, qkv, q, k, v, o, proj, y, norm, fc1, fc2, out: a dozen, each 2^-8 at most and
+    half of that on average) keep the whole within 2 %; an int8 cache adds 1/254 of a head's largest value to k and v."""
+    from bit_ptq_reconstruction_amd import configs, synth
+    from bit_ptq_reconstruction_amd.stream import GROUP, StreamBlock
+
+    T, B = 300, 2
+    weights = {lin.name: synth.weights_torch(lin.N, lin.K, lin.w_seed, dev) for lin in configs.block_linears()}
+    block = StreamBlock(qv, weights, B, T + 20, dev, axes=2, positions=40, base=100.0, int8_cache=int8, frame_tokens=T)
+    g = gen(21)
+    at = torch.randint(0, 40, (T, 2), generator=g, dtype=torch.int32)
+    block.take_frame(torch.randn((T, 1024), generator=g).to(torch.bfloat16).to(dev), 1, at.to(dev))
+    assert block.lens.tolist() == [0, T]
+
+    W = {}
+    for name, lin in block.linears.items():
+        q = torch.from_numpy(oracle.unpack_int4(block.Wq[name].cpu().numpy()).astype(np.float64))
+        W[name] = (q * block.ws[name].cpu().double().repeat_interleave(GROUP, 1)) @ hadamard64(lin.K) / math.sqrt(lin.K)
+    size = block.cache.page_size
+    val = lambda p, s: p.cpu().double() * (1 if s is None else s.cpu().double()[..., None])
+    past = {}
+    for b in range(B):
+        n = int(block.lens[b])
+        t = torch.arange(n)
+        pg, slot = block.table[b].cpu().long()[t // size], t % size
+        past[b] = [val(block.cache.k_pages, block.cache.k_scale)[pg, :, slot], val(block.cache.v_pages, block.cache.v_scale)[pg, :, slot]]
+    norm = lambda x: torch.nn.functional.layer_norm(x, (1024,))
+    turn = lambda x, p: turn32(x.float(), block.cos.cpu(), block.sin.cpu(), p, 2).double()
+    for i in range(3):
+        x = torch.randn((B, 1024), generator=g).to(torch.bfloat16)
+        p = torch.randint(0, 40, (B, 2), generator=g, dtype=torch.int32)
+        block.position.copy_(p.to(dev))
+        out = block.step(x.to(dev)).double().cpu()
+        qkv = (norm(x.double()) @ W["qkv"].t()).view(B, 3, 16, 64)
+        q, k, v = turn(qkv[:, 0], p), turn(qkv[:, 1], p), qkv[:, 2]
+        o = torch.empty((B, 16, 64), dtype=torch.float64)
+        for b in range(B):
+            past[b] = [torch.cat((past[b][0], k[b:b + 1])), torch.cat((past[b][1], v[b:b + 1]))]
+            s = torch.einsum("hd,thd->ht", q[b], past[b][0]) / 8.0
+            o[b] = torch.einsum("ht,thd->hd", torch.softmax(s, -1), past[b][1])
+        y = x.double() + o.view(B, 1024) @ W["proj"].t()
+        h = norm(y) @ W["fc1"].t()
+        expect = y + (h * torch.special.ndtr(h)) @ W["fc2"].t()
+        off = (out - expect).norm().item() / expect.norm().item()
+        assert off <= 0.02, f"step {i}: {off:.3e}"
+    assert block.lens.tolist() == [3, T + 3]
+
+
+def test_stream_example(dev):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "stream_block.py")
+    spec = importlib.util.spec_from_file_location("stream_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    block, out = m.main(["--frames", "1", "--sequences", "2", "--tokens", "5"])
+    assert block.lens.tolist() == [1374 + 6] * 2 and out.shape == (2, 1024)
