@@ -30,6 +30,7 @@
 
 #include <atomic>
 
+#include "fwht_regs.h"
 #include "qv_decode_internal.h"
 
 namespace qv {
@@ -133,10 +134,28 @@ __device__ __forceinline__ bf16x8 widen(unsigned w) {
 
 __device__ __forceinline__ float gelu(float y) { return 0.5f * y * erfcf(-y * 0.70710678118654752f); }
 
+// One butterfly stage across the lanes of a 16-lane row, self + sigma * partner, over 8 registers (see fwht_regs.h).
+#define QV_DPP8(CTRL, R, S)                                                                                       \
+  asm volatile(                                                                                                   \
+      "s_nop 1\n\t"                                                                                               \
+      "v_fmac_f32_dpp %0, %0, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "v_fmac_f32_dpp %1, %1, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "v_fmac_f32_dpp %2, %2, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "v_fmac_f32_dpp %3, %3, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "v_fmac_f32_dpp %4, %4, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "v_fmac_f32_dpp %5, %5, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "v_fmac_f32_dpp %6, %6, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "v_fmac_f32_dpp %7, %7, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                         \
+      "s_nop 1"                                                                                                   \
+      : "+v"(R[0]), "+v"(R[1]), "+v"(R[2]), "+v"(R[3]), "+v"(R[4]), "+v"(R[5]), "+v"(R[6]), "+v"(R[7])            \
+      : "v"(S))
+
 // Sylvester-order Hadamard transform of up to B rows, each by K / 8 threads (t of them counted here), times
-// mult / sqrt(K): log2(K) butterfly stages, three in registers per pass over LDS.  The rows go through the passes
-// together, so that they share the barriers.  What a thread reads from memory is loaded ahead; run() is called
-// by every thread of a block.
+// mult / sqrt(K), into LDS.  A wave holds 512 neighbouring elements, 8 a lane, and runs the stages of their 9 index
+// bits in registers: bits 0-2 in the lane, 3-6 by DPP (the lanes' order and the sign that these stages leave
+// are those of fwht_regs.h), 7 and 8 by changing lane bits 4 and 5 over with register bits 0 and 1.  The row then goes
+// through LDS once and the remaining bits are in registers again.  The rows go side by side, so that they share the
+// two barriers.  What a thread reads from memory is loaded ahead; run() is called by every thread of a block.
 template <int K, typename X, int B>
 struct RotateRows {
   static_assert(K == 1024 || K == 4096, "Hadamard width");
@@ -145,17 +164,20 @@ struct RotateRows {
   Eight<X> e[B];
   float f[8];
 
-  __device__ __forceinline__ void load(int b, const X* __restrict__ x, int t) { load_eight(x + 8 * t, e[b]); }
+  __device__ __forceinline__ void load(int b, const X* __restrict__ x, int t) {
+    load_eight(x + 8 * (chunk_of_lane16(t & 15) | (t & ~15)), e[b]);
+  }
   __device__ __forceinline__ void load_mult(const float* __restrict__ mult, int t) {
+    const float norm = (__builtin_popcount((t >> 3) & 15) & 1) ? -kNorm : kNorm;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = mult ? kNorm * mult[t + j * kStep] : kNorm;
+    for (int j = 0; j < 8; ++j) f[j] = mult ? norm * mult[t + j * kStep] : norm;
   }
 
-  // Butterflies over the index bits of the register number, from bit value `from`.
-  template <int from>
+  // Butterflies over bits of the register number, bit values `from` to `to`.
+  template <int from, int to>
   __device__ __forceinline__ static void butterflies(float (&v)[8]) {
 #pragma unroll
-    for (int h = from; h < 8; h <<= 1) {
+    for (int h = from; h <= to; h <<= 1) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if ((j & h) == 0) {
@@ -169,6 +191,10 @@ struct RotateRows {
 
   // Row b's result at row + b * stride; rows from `count` on are left out (the same in every thread).
   __device__ __forceinline__ void run(float* row, int stride, int count, int t) const {
+    const int lane = t & 63;
+    // element of register 0 after the exchanges; register bits 0, 1, 2 are element bits 7, 8, 2
+    float* const own = row + padded((t & ~63) * 8) + 8 * chunk_of_lane16(lane & 15) + 8 * (chunk_of_lane16(lane & 15) >> 3) +
+                       ((lane >> 4) & 1) + 2 * ((lane >> 5) & 1);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (b >= count) break;
@@ -184,30 +210,33 @@ struct RotateRows {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = e[b].d[i >> 2][i & 3];
       }
-      butterflies<1>(v);  // bits 0-2
-      f32x4* p = reinterpret_cast<f32x4*>(row + b * stride + padded(8 * t));
-      p[0] = f32x4{v[0], v[1], v[2], v[3]};
-      p[1] = f32x4{v[4], v[5], v[6], v[7]};
+      butterflies<1, 4>(v);
+      QV_DPP8("quad_perm:[1,0,3,2]", v, stage_sigma(lane, 0));
+      QV_DPP8("quad_perm:[2,3,0,1]", v, stage_sigma(lane, 1));
+      QV_DPP8("row_ror:8", v, stage_sigma(lane, 2));
+      QV_DPP8("row_mirror", v, stage_sigma(lane, 3));
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const auto x = __builtin_amdgcn_permlane16_swap(float_bits(v[j]), float_bits(v[j + 1]), false, false);
+        const unsigned x0 = x[0], x1 = x[1];
+        v[j] = bits_float(x0);
+        v[j + 1] = bits_float(x1);
+      }
+      butterflies<1, 1>(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j & 2) continue;
+        const auto x = __builtin_amdgcn_permlane32_swap(float_bits(v[j]), float_bits(v[j + 2]), false, false);
+        const unsigned x0 = x[0], x1 = x[1];
+        v[j] = bits_float(x0);
+        v[j + 2] = bits_float(x1);
+      }
+      butterflies<2, 2>(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        own[b * stride + padded(128) * (j & 1) + padded(256) * ((j >> 1) & 1) + 4 * (j >> 2)] = v[j];
     }
     __syncthreads();
-#pragma unroll
-    for (int bit = 3; bit <= 6; bit += 3) {  // bits 3-5, then 6-8: elements a fixed step apart, padding included
-      const int first = padded((t & ((1 << bit) - 1)) + ((t >> bit) << (bit + 3)));
-      constexpr int kSteps[2] = {8, padded(64)};
-      const int step = kSteps[bit / 3 - 1];
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        if (b >= count) break;
-        float* const x = row + b * stride + first;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = x[j * step];
-        butterflies<1>(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j * step] = v[j];
-      }
-      __syncthreads();
-    }
     // bits 9-11 at K = 4096; at K = 1024 only bit 9, the last of the three
 #pragma unroll
     for (int b = 0; b < B; ++b) {
@@ -216,7 +245,7 @@ struct RotateRows {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = x[j * padded(kStep)];
-      butterflies<K == 1024 ? 4 : 1>(v);
+      butterflies<K == 1024 ? 4 : 1, 4>(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j * padded(kStep)] = v[j] * f[j];
     }
