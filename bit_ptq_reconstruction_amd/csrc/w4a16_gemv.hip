@@ -48,8 +48,7 @@ constexpr int kWindow = 128;  // codes of a window: one 16-byte load by each qua
 
 // Variants by size (see the rules' measurements below).
 constexpr int kNarrow = 16 * 256;  // channels that one block of 16 on every CU takes
-constexpr int kFewRows = 4;        // rows up to which lanes read activations directly
-constexpr int kFused1024 = 12, kFused4096 = 4;  // rows up to which every block rotates them by itself
+constexpr int kFused1024 = 12, kFused4096 = 5;  // rows up to which every block rotates them by itself
 
 // Rotated rows lie in LDS as floats with 8 floats of padding after every 64, so that the strided reads
 // of the transform's passes and the fragment reads of the four quarters fall in different banks.
@@ -151,11 +150,11 @@ __device__ __forceinline__ float gelu(float y) { return 0.5f * y * erfcf(-y * 0.
       : "v"(S))
 
 // Sylvester-order Hadamard transform of up to B rows, each by K / 8 threads (t of them counted here), times
-// mult / sqrt(K), into LDS.  A wave holds 512 neighbouring elements, 8 a lane, and runs the stages of their 9 index
+// mult / sqrt(K).  A wave holds 512 neighbouring elements, 8 a lane, and runs the stages of their 9 index
 // bits in registers: bits 0-2 in the lane, 3-6 by DPP (the lanes' order and the sign that these stages leave
 // are those of fwht_regs.h), 7 and 8 by changing lane bits 4 and 5 over with register bits 0 and 1.  The row then goes
 // through LDS once and the remaining bits are in registers again.  The rows go side by side, so that they share the
-// two barriers.  What a thread reads from memory is loaded ahead; run() is called by every thread of a block.
+// barriers.  What a thread reads from memory is loaded ahead; run() is called by every thread of a block.
 template <int K, typename X, int B>
 struct RotateRows {
   static_assert(K == 1024 || K == 4096, "Hadamard width");
@@ -189,8 +188,10 @@ struct RotateRows {
     }
   }
 
-  // Row b's result at row + b * stride; rows from `count` on are left out (the same in every thread).
-  __device__ __forceinline__ void run(float* row, int stride, int count, int t) const {
+  // Row b goes through LDS at row + b * stride; put(b, k, x) takes its results.  Rows from `count` on are left out (the
+  // same in every thread).
+  template <typename Put>
+  __device__ __forceinline__ void run(float* row, int stride, int count, int t, Put put) const {
     const int lane = t & 63;
     // element of register 0 after the exchanges; register bits 0, 1, 2 are element bits 7, 8, 2
     float* const own = row + padded((t & ~63) * 8) + 8 * chunk_of_lane16(lane & 15) + 8 * (chunk_of_lane16(lane & 15) >> 3) +
@@ -238,19 +239,37 @@ struct RotateRows {
     }
     __syncthreads();
     // bits 9-11 at K = 4096; at K = 1024 only bit 9, the last of the three
+    float v[B][8];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (b >= count) break;
-      float* const x = row + b * stride + padded(t);
-      float v[8];
+      const float* const x = row + b * stride + padded(t);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = x[j * padded(kStep)];
-      butterflies<K == 1024 ? 4 : 1, 4>(v);
+      for (int j = 0; j < 8; ++j) v[b][j] = x[j * padded(kStep)];
+      butterflies<K == 1024 ? 4 : 1, 4>(v[b]);
+    }
+    __syncthreads();  // the pieces may take the rows' place
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j * padded(kStep)] = v[j] * f[j];
+    for (int b = 0; b < B; ++b) {
+      if (b >= count) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) put(b, t + j * kStep, v[b][j] * f[j]);
     }
   }
 };
+
+// The NP pieces of activation k of a row, where the codes' order wants them: elements s and s + 4 of eight are neighbours.
+// Piece p of the row lies p * stride further.
+template <int NP>
+__device__ __forceinline__ void put_pieces(uint16_t* row, int stride, int k, float x) {
+  uint16_t* const to = row + (k & ~7) + 2 * (k & 3) + ((k >> 2) & 1);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const unsigned u = float_bits(x);
+    to[p * stride] = (uint16_t)(u >> 16);
+    x -= bits_float(u & 0xFFFF0000u);  // exact: the piece is the value's top bits
+  }
+}
 
 template <typename X>
 struct Args {
@@ -265,16 +284,23 @@ struct Args {
   int gelu, y_bf16;
 };
 
-// EXACT: fp32 results, codes converted exactly.  NT: tiles of 16 channels of a block; with fewer of them a
-// wave holds more windows in flight instead, 4 loads of 16 bytes a lane in all.
-// SRC: where a wave's fragments of the rows come from.
+// EXACT: fp32 results, codes converted exactly.
+// NT: tiles of 16 channels of a block.  S: with few channels a tile has 16 / S of them and a load S windows, so that
+// more blocks share the codes.
+// SRC: where a wave's operands of the rows come from.
 enum Source {
-  kDirect,  // memory: a lane reads its own 32 activations of a window (few rows: few cache lines an instruction)
-  kStaged,  // memory, through an LDS region of the wave's own, so that a row's window is read in one piece
+  kStaged,            // memory, through an LDS region of the wave's own, so that a row's window is read in one piece
   kRot1024, kRot4096  // LDS: the block rotates its rows into it first
 };
 template <int SRC>
 constexpr int kWidth = SRC == kRot1024 ? 1024 : (SRC == kRot4096 ? 4096 : 0);
+
+// LDS that a rotated row takes: as floats on its way, as pieces of K + 8 values in the end (the padding keeps 16 rows'
+// operands in different banks).
+template <int K, int NP>
+__host__ __device__ constexpr int rotated_bytes() {
+  return NP * (K + 8) * 2 > padded(K) * 4 ? NP * (K + 8) * 2 : padded(K) * 4;
+}
 
 // Rows that a block's rotation writes: at K = 1024 it takes four at a time.
 template <int K>
@@ -282,21 +308,25 @@ __host__ __device__ constexpr int rotated_rows(int rows) {
   return K == 1024 ? (rows + 3) & ~3 : rows;
 }
 
-template <typename X, int NP, bool EXACT, int NT, int SRC>
+template <typename X, int NP, bool EXACT, int NT, int S, int SRC>
 __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
-  constexpr int kDepth = NT == 1 ? 4 : 2;  // windows in flight
+  static_assert(NT == 1 || S == 1, "few channels or many");
+  constexpr int kDepth = NT == 1 ? 4 : 2;  // loads in flight of each tile
+  constexpr int kChannels = 16 / S;        // of a tile
   constexpr int K = kWidth<SRC>;
   extern __shared__ f32x4 lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, c = lane >> 4;
-  const int n0 = blockIdx.x * (16 * NT);
+  const int sub = S == 1 ? 0 : r / kChannels;  // which of S windows this lane loads
+  const int n0 = blockIdx.x * (kChannels * NT);
   const int64_t m0 = (int64_t)blockIdx.y * kRows;
   const int rows = (int)(a.M - m0 < kRows ? a.M - m0 : kRows);
   const int windows = a.K / kWindow, groups = a.K / a.group;
   // Rotation: `kAtOnce` rows side by side, as often as there are rows.
-  constexpr int kAtOnce = K ? 8 * kThreads / K : 1, kBatch = kAtOnce == 1 ? kFused4096 : (kFused1024 + 3) / 4;
-  const int part = K ? threadIdx.x / (K / 8) : 0, in_row = K ? threadIdx.x % (K / 8) : 0;
-  RotateRows<K ? K : 1024, X, kBatch> rotation;
+  constexpr int kHadamard = K ? K : 1024;  // unused without a rotation
+  constexpr int kAtOnce = 8 * kThreads / kHadamard, kBatch = kAtOnce == 1 ? kFused4096 : (kFused1024 + 3) / 4;
+  const int part = threadIdx.x / (kHadamard / 8), in_row = threadIdx.x % (kHadamard / 8);
+  RotateRows<kHadamard, X, kBatch> rotation;
   if constexpr (K != 0) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -307,7 +337,7 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   }
 
   // A wave's windows follow each other, so that both halves of a 128-byte line are asked for together.
-  const int share = (windows + kWaves - 1) / kWaves;
+  const int share = (windows + S * kWaves - 1) / (S * kWaves) * S;
   const int begin = wave * share, end = begin + share < windows ? begin + share : windows;
 
   const uint8_t* const wbase = a.wq + (int64_t)n0 * (a.K / 2);
@@ -315,58 +345,63 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   uint32_t wrow[NT], srow[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int n = n0 + 16 * t + r < a.N ? 16 * t + r : a.N - 1 - n0;
+    const int in_tile = S == 1 ? r : r % kChannels;
+    const int n = n0 + 16 * t + in_tile < a.N ? 16 * t + in_tile : a.N - 1 - n0;
     wrow[t] = (uint32_t)n * (a.K / 2) + 16 * c;
     srow[t] = (uint32_t)n * groups;
   }
   u32x4 w[kDepth][NT];
   auto load_codes = [&](int d, int win) {
+    const int mine = S == 1 || win + sub < windows ? win + sub : windows - 1;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      w[d][t] = *reinterpret_cast<const u32x4*>(wbase + wrow[t] + (uint32_t)win * (kWindow / 2));
+      w[d][t] = *reinterpret_cast<const u32x4*>(wbase + wrow[t] + (uint32_t)mine * (kWindow / 2));
   };
-  // Scales of four windows at a time: quarter c of the wave loads those of window first + c.
+  // Scales of 4 S windows at a time: quarter c of the wave loads those of the load first + c.
   float s[NT];
   auto load_scales = [&](int first) {
-    const int win = first + c < end ? first + c : end - 1;
-    const uint32_t g = (uint32_t)(win * kWindow) >> a.group_shift;
+    const int win = first + S * c + sub;
+    const uint32_t g = (uint32_t)((win < end ? win : end - 1) * kWindow) >> a.group_shift;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) s[t] = sbase[srow[t] + g];
+    for (int t = 0; t < NT; ++t) s[t] = S == 1 || win < end ? sbase[srow[t] + g] : 0.0f;
   };
   if (begin < end) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
-      if (begin + d < end) load_codes(d, begin + d);
+      if (begin + d * S < end) load_codes(d, begin + d * S);
     load_scales(begin);
   }
 
-  float* const rot = reinterpret_cast<float*>(lds);
-  constexpr int kRowFloats = K ? padded(K) : 1;
-  if constexpr (K != 0)
-    rotation.run(rot + part * kRowFloats, kAtOnce * kRowFloats, (rows + kAtOnce - 1) / kAtOnce, in_row);
+  char* const room = reinterpret_cast<char*>(lds);
+  constexpr int kPieceRow = K + 8;
+  uint16_t* const split_rows = reinterpret_cast<uint16_t*>(room);
+  if constexpr (K != 0) {
+    rotation.run(reinterpret_cast<float*>(room) + part * padded(K), kAtOnce * padded(K), (rows + kAtOnce - 1) / kAtOnce,
+                 in_row, [&](int b, int k, float x) {
+                   put_pieces<NP>(split_rows + (b * kAtOnce + part) * NP * kPieceRow, kPieceRow, k, x);
+                 });
+  }
   const int row = r < rows ? r : rows - 1;
-  const X* const xrow = a.x + (m0 + row) * a.ldx + 32 * c;
-  const float* const lrow = rot + row * kRowFloats;
 
   // Staged rows: a wave reads its window of every row in one piece, 16 bytes a lane, and holds the next
   // one while it works; 16 bytes of padding a row keep the 16 rows' fragments in different banks.
-  constexpr int kPerLoad = 16 / (int)sizeof(X);                      // activations
-  constexpr int kLanesPerRow = kWindow / kPerLoad;                   // 16 (bf16) or 32 (fp32)
-  constexpr int kLoads = kRows * kLanesPerRow / 64;                  // 4 or 8
-  constexpr int kStageRow = kWindow + kPerLoad;                      // activations
-  X* const stage = reinterpret_cast<X*>(rot) + wave * (kRows * kStageRow);
-  u32x4 xs[SRC == kStaged ? kLoads : 1];
+  constexpr int kPerLoad = 16 / (int)sizeof(X);      // activations
+  constexpr int kLanesPerRow = kWindow / kPerLoad;   // 16 (bf16) or 32 (fp32)
+  constexpr int kRowsPerLoad = 64 / kLanesPerRow;
+  constexpr int kLoads = kRows / kRowsPerLoad;
+  constexpr int kStageRow = kWindow + kPerLoad;      // activations
+  X* const stage = reinterpret_cast<X*>(room) + wave * (rows * kStageRow);
+  const int stage_row = lane / kLanesPerRow, stage_k = (lane % kLanesPerRow) * kPerLoad;
+  u32x4 xs[K == 0 ? kLoads : 1];
   auto load_stage = [&](int win) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      if (i * (64 / kLanesPerRow) >= rows) break;
-      const int m = i * (64 / kLanesPerRow) + lane / kLanesPerRow;
-      const int from = m < rows ? m : rows - 1;
-      xs[i] = *reinterpret_cast<const u32x4*>(a.x + (m0 + from) * a.ldx + win * kWindow +
-                                              (lane % kLanesPerRow) * kPerLoad);
+      if (i * kRowsPerLoad >= rows) break;
+      const int m = i * kRowsPerLoad + stage_row;
+      xs[i] = *reinterpret_cast<const u32x4*>(a.x + (m0 + (m < rows ? m : rows - 1)) * a.ldx + win * kWindow + stage_k);
     }
   };
-  if constexpr (SRC == kStaged) {
+  if constexpr (K == 0) {
     if (begin < end) load_stage(begin);
   }
   if constexpr (K != 0) __syncthreads();
@@ -382,12 +417,12 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   bf16x8 xf[4][NP];
   f32x4 sum;
   auto take_rows = [&](int win) {
-    if constexpr (SRC == kStaged) {
+    if constexpr (K == 0) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        if (i * (64 / kLanesPerRow) >= rows) break;
-        const int m = i * (64 / kLanesPerRow) + lane / kLanesPerRow;
-        *reinterpret_cast<u32x4*>(stage + m * kStageRow + (lane % kLanesPerRow) * kPerLoad) = xs[i];
+        if (i * kRowsPerLoad >= rows) break;
+        const int m = i * kRowsPerLoad + stage_row;
+        if (m < rows) *reinterpret_cast<u32x4*>(stage + m * kStageRow + stage_k) = xs[i];
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -397,16 +432,16 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (K != 0) {
-        Eight<float> e;
-        load_eight(lrow + padded(win * kWindow + 32 * c) + 8 * j, e);
-        pieces<NP>(e, xf[j]);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          xf[j][p] = *reinterpret_cast<const bf16x8*>(split_rows + (row * NP + p) * kPieceRow + win * kWindow + 32 * c + 8 * j);
       } else {
         Eight<X> e;
-        load_eight(SRC == kStaged ? stage + row * kStageRow + 32 * c + 8 * j : xrow + win * kWindow + 8 * j, e);
+        load_eight(stage + row * kStageRow + 32 * c + 8 * j, e);
         pieces<NP>(e, xf[j]);
       }
     }
-    if constexpr (SRC == kStaged) __builtin_amdgcn_wave_barrier();
+    if constexpr (K == 0) __builtin_amdgcn_wave_barrier();
     sum = f32x4{0, 0, 0, 0};
     if constexpr (!EXACT) {
 #pragma unroll
@@ -430,28 +465,53 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
     for (int i = 0; i < 4; ++i) to[i] += EXACT ? 16.0f * f * acc[i] : f * (acc[i] - 24.0f * sum[i]);
   };
 
-  for (int first = begin; first < end; first += 4) {
+  for (int first = begin; first < end; first += 4 * S) {
     float sc[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) sc[t] = s[t];
-    if (first + 4 < end) load_scales(first + 4);
+    if (first + 4 * S < end) load_scales(first + 4 * S);
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const int win = first + d;
+      const int win = first + d * S;
       if (win >= end) break;
-      take_rows(win);
       f32x4 acc[NT];
+      if constexpr (S == 1) {
+        take_rows(win);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t] = product(w[d % kDepth][t]);
-      if (win + kDepth < end) load_codes(d % kDepth, win + kDepth);
+        for (int t = 0; t < NT; ++t) acc[t] = product(w[d % kDepth][t]);
+      } else {
+        // A load's columns belong to S windows: each window's product is taken with all of them and its own are kept.
+        bf16x8 wf[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wf[j] = EXACT ? widen_exact(w[d][0][j]) : widen(w[d][0][j]);
+        f32x4 own = {0, 0, 0, 0};
+        acc[0] = own;
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+          if (win + u >= end) break;
+          take_rows(win + u);
+          f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], wf[j], x, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[0][i] = sub == u ? x[i] : acc[0][i];
+            own[i] = sub == u ? sum[i] : own[i];
+          }
+        }
+        sum = own;
+      }
+      if (win + kDepth * S < end) load_codes(d % kDepth, win + kDepth * S);
 #pragma unroll
       for (int t = 0; t < NT; ++t) add(y[t], __shfl(sc[t], r + 16 * d), acc[t]);
     }
   }
 
   // Element (m, n) of tile t at [wave][t][m][n].
-  if constexpr (SRC == kStaged) __syncthreads();  // the sums take the staging regions' place
-  float* const red = rot + (K ? rotated_rows<K>(rows) * kRowFloats : 0);
+  if constexpr (K == 0) __syncthreads();  // the sums take the staging regions' place
+  float* const red = reinterpret_cast<float*>(room + (K ? rotated_rows<K>(rows) * rotated_bytes<K, NP>() : 0));
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -459,10 +519,12 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   __syncthreads();
   for (int idx = threadIdx.x; idx < 256 * NT; idx += kThreads) {
     const int t = idx >> 8, m = (idx >> 4) & 15, n = n0 + 16 * t + (idx & 15);
-    if (m >= rows || n >= a.N) continue;
+    if (m >= rows || n >= a.N || (S > 1 && (idx & 15) >= kChannels)) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += red[k * NT * 256 + idx];
+    for (int k = 0; k < kWaves; ++k)
+#pragma unroll
+      for (int u = 0; u < S; ++u) v += red[k * NT * 256 + idx + u * kChannels];
     if (a.bias) v += a.bias[n];
     if (a.gelu) v = gelu(v);
     const int64_t at = (m0 + m) * a.ldy + n;
@@ -478,28 +540,27 @@ template <int K, typename X>
 __global__ __launch_bounds__(K / 8) void rotate_rows_kernel(const X* __restrict__ x, int64_t ldx,
                                                             const float* __restrict__ mult, float* __restrict__ out) {
   __shared__ f32x4 row4[padded(K) / 4];
-  float* row = reinterpret_cast<float*>(row4);
   const int t = threadIdx.x;
   RotateRows<K, X, 1> rotation;
   rotation.load(0, x + (int64_t)blockIdx.x * ldx, t);
   rotation.load_mult(mult, t);
-  rotation.run(row, 0, 1, t);
-  __syncthreads();
-  f32x4* o = reinterpret_cast<f32x4*>(out + (int64_t)blockIdx.x * K + 8 * t);
-  const f32x4* p = reinterpret_cast<const f32x4*>(row + padded(8 * t));
-  o[0] = p[0];
-  o[1] = p[1];
+  float* const to = out + (int64_t)blockIdx.x * K;
+  rotation.run(reinterpret_cast<float*>(row4), 0, 1, t, [&](int, int k, float v) { to[k] = v; });
 }
 
-template <typename X, int NP, bool EXACT, int NT, int SRC>
+template <typename X, int NP, bool EXACT, int NT, int S, int SRC>
 hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
   constexpr int K = kWidth<SRC>;
-  const unsigned gx = (unsigned)((a.N + 16 * NT - 1) / (16 * NT));
+  constexpr int kBlock = 16 / S * NT;  // channels
+  const unsigned gx = (unsigned)((a.N + kBlock - 1) / kBlock);
   const int rows = (int)(a.M < kRows ? a.M : kRows);
   size_t bytes = (size_t)kWaves * NT * 256 * 4;
-  if (K) bytes += (size_t)rotated_rows<K>(rows) * padded(K) * 4;
-  const size_t staged = (size_t)kWaves * kRows * (kWindow * sizeof(X) + 16);
-  if (SRC == kStaged && bytes < staged) bytes = staged;
+  if (K) {
+    bytes += (size_t)rotated_rows<K>(rows) * rotated_bytes<K, NP>();
+  } else {
+    const size_t staged = (size_t)kWaves * rows * (kWindow * sizeof(X) + 16);
+    if (bytes < staged) bytes = staged;
+  }
   if (bytes > 65536) {
     static std::atomic<uint64_t> raised{0};  // a bit for each device whose limit was raised for this kernel
     int dev = 0;
@@ -507,7 +568,7 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
     if (e != hipSuccess) return e;
     const uint64_t bit = uint64_t{1} << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&w4a16_kernel<X, NP, EXACT, NT, SRC>),
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&w4a16_kernel<X, NP, EXACT, NT, S, SRC>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
       if (e != hipSuccess) return e;
       raised.fetch_or(bit, std::memory_order_relaxed);
@@ -520,7 +581,7 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
     b.x += m * a.ldx;
     b.M = a.M - m < step ? a.M - m : step;
     b.y = static_cast<char*>(a.y) + m * a.ldy * (a.y_bf16 ? 2 : 4);
-    w4a16_kernel<X, NP, EXACT, NT, SRC>
+    w4a16_kernel<X, NP, EXACT, NT, S, SRC>
         <<<dim3(gx, (unsigned)((b.M + kRows - 1) / kRows)), kThreads, bytes, st>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -530,11 +591,13 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
 
 template <typename X, int NP, bool EXACT, int SRC>
 hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
-  if constexpr (SRC != kDirect) {  // the callers' rule: few rows and few channels
-    if (a.N > 2 * kNarrow) return launch_kernel<X, NP, EXACT, 4, SRC>(a, st);
-    if (a.N > kNarrow) return launch_kernel<X, NP, EXACT, 2, SRC>(a, st);
+  if (a.N > 2 * kNarrow) return launch_kernel<X, NP, EXACT, 4, 1, SRC>(a, st);
+  if (a.N > kNarrow) return launch_kernel<X, NP, EXACT, 2, 1, SRC>(a, st);
+  if constexpr (SRC != kRot1024) {  // with 8 windows, one for each wave
+    if (a.K >= 4 * kWaves * kWindow && a.N <= kNarrow / 4) return launch_kernel<X, NP, EXACT, 1, 4, SRC>(a, st);
+    if (a.K >= 2 * kWaves * kWindow && a.N <= kNarrow / 2) return launch_kernel<X, NP, EXACT, 1, 2, SRC>(a, st);
   }
-  return launch_kernel<X, NP, EXACT, 1, SRC>(a, st);
+  return launch_kernel<X, NP, EXACT, 1, 1, SRC>(a, st);
 }
 
 // Pieces by the types: rows that are bf16 are one piece; others two or, for fp32 results, three.
@@ -547,29 +610,19 @@ hipError_t by_types(const Args<X>& a, hipStream_t st) {
 }
 
 template <typename X>
-hipError_t rotate_rows(const X* x, int64_t M, int64_t K, int64_t ldx, const float* mult, float* out, hipStream_t st) {
-  if (K == 1024)
-    rotate_rows_kernel<1024, X><<<(unsigned)M, 128, 0, st>>>(x, ldx, mult, out);
-  else
-    rotate_rows_kernel<4096, X><<<(unsigned)M, 512, 0, st>>>(x, ldx, mult, out);
-  return hipGetLastError();
-}
-
-template <typename X>
-hipError_t unrotated(const Args<X>& a, hipStream_t st) {
-  return a.M > kFewRows || a.N > kNarrow ? by_types<X, kStaged>(a, st) : by_types<X, kDirect>(a, st);
-}
-
-template <typename X>
-hipError_t launch(Args<X> a, bool rotate, float* rows32, hipStream_t st) {
-  if (!rotate) return unrotated<X>(a, st);
+hipError_t launch(const Args<X>& a, bool rotate, float* rows32, hipStream_t st) {
+  if (!rotate) return by_types<X, kStaged>(a, st);
   if (a.K == 1024 && a.M <= kFused1024) return by_types<X, kRot1024>(a, st);
   if (a.K == 4096 && a.M <= kFused4096) return by_types<X, kRot4096>(a, st);
-  const hipError_t e = rotate_rows<X>(a.x, a.M, a.K, a.ldx, a.mult, rows32, st);
+  if (a.K == 1024)
+    rotate_rows_kernel<1024, X><<<(unsigned)a.M, 128, 0, st>>>(a.x, a.ldx, a.mult, rows32);
+  else
+    rotate_rows_kernel<4096, X><<<(unsigned)a.M, 512, 0, st>>>(a.x, a.ldx, a.mult, rows32);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const Args<float> b = {rows32, nullptr, a.wq, a.ws, a.bias, a.y, a.M, a.K, a.ldy, a.N, a.K, a.group,
                          a.group_shift, a.gelu, a.y_bf16};
-  return unrotated<float>(b, st);
+  return by_types<float, kStaged>(b, st);
 }
 
 }  // namespace

@@ -48,7 +48,7 @@ size_t qv_w4a16_linear_workspace_size(int64_t M, int64_t K);
 
 /*
  * qv_w4a16_linear -- the online layer with 4-bit weights and unquantized activations: the rows are
- * rotated and smoothed as in qv_hadamard_smooth_quant, kept in fp32, and multiplied as in qv_w4a16_gemv.
+ * rotated and smoothed in fp32 as in qv_hadamard_smooth_quant and multiplied as in qv_w4a16_gemv.
  *   K           1024 or 4096.   inv_smooth  [K] fp32, NULL = ones.
  *   workspace   at least qv_w4a16_linear_workspace_size(M, K) bytes, 256-byte aligned, reused freely.
  */
