@@ -524,15 +524,14 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
   }
 }
 
-// Parts joined: one block to a query head.  Its threads first weigh the parts, then kJoin / D groups of D threads
-// add every so-many-th part, several loads in flight each.
-constexpr int kJoin = 512;
+// Parts joined: one block to a query head.  Every wave weighs all parts by itself (lane p of 64 at a time), adds every
+// kJoinWaves-th of them, several loads in flight, and the waves' sums meet once in LDS.
+constexpr int kJoinWaves = 8;
 template <int D, typename X>
-__global__ __launch_bounds__(kJoin) void join_kernel(Args a) {
-  constexpr int kGroups = kJoin / D;
-  __shared__ float weight[kManyBlocks + 1];
-  __shared__ float red[kJoin / 64];
-  __shared__ float sums[kGroups][D];
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
+  constexpr int kPer = D / 64;  // channels of a lane
+  __shared__ float sums[kJoinWaves][D];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t b = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
   const Part part = find_part<false>(a, (int)b);
   const int parts = part.count;
@@ -540,38 +539,39 @@ __global__ __launch_bounds__(kJoin) void join_kernel(Args a) {
   const int64_t at = (int64_t)part.first_of * a.q_heads + head;
   const int64_t step = a.q_heads;
   const float* const ml = a.partial + (int64_t)a.parts * a.q_heads * D + 2 * at;
-  auto across = [&](float x, auto op) {  // over the block
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x = op(x, __shfl_xor(x, d));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = red[0];
-#pragma unroll
-    for (int w = 1; w < kJoin / 64; ++w) x = op(x, red[w]);
-    return x;
-  };
-  float m = kLowest, l = 0.0f;
-  for (int p = threadIdx.x; p < parts; p += kJoin) m = fmaxf(m, ml[2 * p * step]);
-  m = across(m, [](float x, float y) { return fmaxf(x, y); });
-  for (int p = threadIdx.x; p < parts; p += kJoin) {
-    weight[p] = exp2_raw(ml[2 * p * step] - m);
-    l += weight[p] * ml[2 * p * step + 1];
-  }
-  l = across(l, [](float x, float y) { return x + y; });  // and the weights are written
+  const float* const val = a.partial + at * D + kPer * lane;
 
-  const int g = threadIdx.x / D, d = threadIdx.x % D;
-  const float* const val = a.partial + at * D + d;
-  float o = 0.0f;
-#pragma unroll 8
-  for (int p = g; p < parts; p += kGroups) o += weight[p] * val[p * step * D];
-  sums[g][d] = o;
-  __syncthreads();
-  if (threadIdx.x < D) {
-    o = sums[0][d];
+  float m = kLowest, l = 0.0f, o[kPer];
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) o += sums[i][d];
-    store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, l > 0.0f ? o / l : 0.0f);
+  for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
+  for (int first = 0; first < parts; first += 64) {
+    const int p = first + lane, n = parts - first < 64 ? parts - first : 64;
+    const float pm = p < parts ? ml[2 * p * step] : kLowest, pl = p < parts ? ml[2 * p * step + 1] : 0.0f;
+    float top = fmaxf(m, pm);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float shrink = exp2_raw(m - top), weight = p < parts ? exp2_raw(pm - top) : 0.0f;
+    m = top;
+    l = l * shrink + weight * pl;  // of this lane's parts
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] *= shrink;
+#pragma unroll 8
+    for (int q = wave; q < n; q += kJoinWaves) {
+      const float w = bits_float(__builtin_amdgcn_readlane(float_bits(weight), q));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] += w * val[(first + q) * step * D + i];
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sums[wave][kPer * lane + i] = o[i];
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += 64 * kJoinWaves) {
+    float x = sums[0][d];
+#pragma unroll
+    for (int w = 1; w < kJoinWaves; ++w) x += sums[w][d];
+    store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, l > 0.0f ? x / l : 0.0f);
   }
 }
 
@@ -584,7 +584,7 @@ hipError_t launch(const Args& a, bool split, hipStream_t st) {
     attention_kernel<D, X, INT8, false, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !split) return e;
-  join_kernel<D, X><<<a.B * a.q_heads, kJoin, 0, st>>>(a);
+  join_kernel<D, X><<<a.B * a.q_heads, 64 * kJoinWaves, 0, st>>>(a);
   return hipGetLastError();
 }
 
