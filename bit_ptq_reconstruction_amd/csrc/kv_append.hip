@@ -5,7 +5,9 @@
 //   int8: scale = max |x'| / 127 over the head's channels, code = clamp(rne(x' / scale))
 //
 // Each value is read once and written once with a few operations between, so the kernel is bound by
-// memory.  A thread holds 8 low and 8 high channels of one head of one token: both sides of its 8
+// memory: 10992 tokens of 48 heads of 64 (138 MB with the tables) take 32 us, 4.3 TB/s against a copy's 5.0; one token of each of 24
+// sequences takes 3.2 us, a launch; 1833 fp32 tokens into int8 (40 MB) 12 us, 3.4 TB/s, part of it the exact quotients.
+// A thread holds 8 low and 8 high channels of one head of one token: both sides of its 8
 // pairs, in 16-byte loads and stores.  The D / 16 threads of a head are neighbours in a wave, so the int8
 // scale is a maximum over 4 or 8 lanes.
 //

@@ -3,22 +3,33 @@
 //
 //   O[b][i] = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q_i . k_t - m),  m the running maximum
 //
-// One pass over the keys and values, which is all there is to move: the kernel is bound by memory.  The
-// length is split into parts over the grid so that few sequences still fill the chip, and a second
-// kernel joins the parts by their maxima and sums.
+// One pass over the keys and values, which is all there is to move: the kernel is bound by memory.  48 sequences of up to
+// 16384 tokens (8 heads of 128, 32 queries, 1.6 GB) take 271 us, 6.0 TB/s (a copy runs at 5.0; the matrix cores are busy for 6 %
+// and the vector ALU for 13 % of the time); two of 99991 tokens in int8 (211 MB) take 49-51 us, 4.2 TB/s (vector ALU
+// 41 %, for the conversions).  One frame of 1374 tokens (5.6 MB) takes 7.9 us: 5.0 for the parts' chain of loads (lengths,
+// page table, keys) and 2.9 for the join.
 //
-// A wave takes 16 tokens a tile and the up to 16 query heads that share a cache head, and nothing leaves
-// its registers between the two products:
-//   S^T = K q^T   v_mfma_f32_16x16x32_bf16: lane (r = lane % 16, c = lane / 16) loads 16 bytes of token r's
-//                 key as they lie in memory; it gets the scores of tokens 4 c + i (i < 4) for query r.
-//   O^T += V^T P^T  v_mfma_f32_16x16x4f32: step i contracts the four tokens 4 c + i, so lane (r, c)'s score
-//                 number i already is the operand, unrounded, and the other operand is value
-//                 channel D / 16 r + e of token 4 c + i: D / 16 neighbouring channels of one token,
-//                 one load.  The result has query r in lane (r, c), channels 4 D / 16 c onwards, next to
-//                 that query's maximum and sum.
-// The order of channels inside S and of tokens inside O is free, which is what makes both loads contiguous.
-// With one query per cache head 15 of 16 columns repeat it; the matrix cores have the room (at D =
-// 128 and bf16 a tile's 32 + 4 MFMAs take about a third of the time its 8 KB take to arrive).
+// A wave takes two tiles of 16 tokens at a time and the up to 16 query heads that share a cache head, and nothing leaves its
+// registers between the two products:
+//   S^T = K q^T     lane (r = lane % 16, c = lane / 16) loads 16 bytes of token r's key as they lie in memory; it gets
+//                   the scores of tokens 4 c + i (i < 4) for query r.
+//   O^T += V^T P^T  over 32 tokens, slots 8 c + 4 u + i being token 4 c + i of tile u: so a lane's own scores are its operand,
+//                   in bf16 pieces that sum to them (two pieces, 16 bits, for bf16 results, three for fp32; one piece's
+//                   2^-9 would show).  The other operand is value channel D / 16 r + e of the same tokens: each lane
+//                   loads D / 16 neighbouring channels of four tokens a tile and picks channel e of a pair of tokens with one
+//                   byte permutation.  The result has query r in lane (r, c), channels 4 D / 16 c onwards, next
+//                   to that query's maximum and sum.
+// Both are v_mfma_f32_16x16x32_bf16.  The order of channels inside S and of tokens inside O is free, which is what makes the
+// loads contiguous and saves any exchange between lanes.  (v_mfma_f32_16x16x4_f32 takes P unrounded and needs no pieces, but
+// four times the matrix time: long int8 86 against 74 us when it was tried, large batch 300 against 278.)
+// With one query to a head its probabilities stand in all 16 columns, so that every lane has those of its tokens, and the
+// second product is D / 16 fp32 multiply-adds a token.
+// The next unit's keys are loaded as soon as this one's scores are formed, its values as soon as this one's sum is.
+//
+// The tokens of all sequences together are cut into parts of equal size, one round of blocks (kFewBlocks), or more where
+// each part still has kLongPart tokens; a second kernel joins a sequence's parts by their maxima and sums.  Measured
+// with 768, 1024 and 1536 blocks: ragged batch 61, 61, 59 us, long int8 49, 56, 56 (512 blocks: 71 and 58 where 768 took 64 and 54);
+// kLongPart of 768, 1536 and 3072 tokens: long int8 60, 54, 54, large batch 279, 278, 293.
 #include <hip/hip_bf16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -627,10 +638,14 @@ hipError_t launch_paged_attention(const AttentionArgs& in, hipStream_t st) {
   a.scale = in.scale * kLog2e;
   const bool q8 = c.dtype == QV_KV_INT8;
   if (c.head_dim == 64) {
-    if (in.bf16) return q8 ? launch<64, __hip_bfloat16, true>(a, parts.split, st) : launch<64, __hip_bfloat16, false>(a, parts.split, st);
+    if (in.bf16)
+      return q8 ? launch<64, __hip_bfloat16, true>(a, parts.split, st)
+                : launch<64, __hip_bfloat16, false>(a, parts.split, st);
     return q8 ? launch<64, float, true>(a, parts.split, st) : launch<64, float, false>(a, parts.split, st);
   }
-  if (in.bf16) return q8 ? launch<128, __hip_bfloat16, true>(a, parts.split, st) : launch<128, __hip_bfloat16, false>(a, parts.split, st);
+  if (in.bf16)
+    return q8 ? launch<128, __hip_bfloat16, true>(a, parts.split, st)
+              : launch<128, __hip_bfloat16, false>(a, parts.split, st);
   return q8 ? launch<128, float, true>(a, parts.split, st) : launch<128, float, false>(a, parts.split, st);
 }
 

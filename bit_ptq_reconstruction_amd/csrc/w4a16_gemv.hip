@@ -3,8 +3,12 @@
 //
 //   Y[m][n] = sum_g s[n][g] * (sum_{k in g} x[m][k] q[n][k]) (+ bias) (+ GELU),  q in [-8, 7]
 //
-// With a few rows the weights' N K / 2 bytes are all there is to move, so the kernel is bound by memory
-// (by latency for the smallest layers); the arithmetic only has to keep up with it.
+// With a few rows the weights' N K / 2 bytes are all there is to move.  Small layers are bound by latency (a 1024 x
+// 1024 layer takes 3.1 us unrotated and 4.5 us rotated for one row, in a graph whose empty nodes take about 2.5), large
+// ones by the cache-line requests of a CU: 16 rows x 8192 x 16384 take 19-21 us, 72 MB at 3.5-3.7 TB/s (a copy's rate, 5.0
+// TB/s, would be 14.4 us and the launch).  There, without the scales' loads the kernel was 10 % faster, without the rows'
+// 10 %, with codes read in pieces of 1 KB 10 %, while more loads in flight (two or four windows instead of one) changed
+// nothing; hence fewer and fuller requests below.
 //
 // Products run on the matrix cores, 16 rows x 16 channels x 32 codes at a time, whatever M is: one
 // v_mfma_f32_16x16x32_bf16 replaces 512 multiply-adds for 16 cycles, and the vector ALU is left with
@@ -13,17 +17,22 @@
 //     of two are packed: 19 instructions for 8 codes).
 //   - with bf16 results a code q becomes 24 + q in [16, 31], i.e. the bits 0x4180 | (q + 8) << 3: one shift
 //     and one and-or for two codes, 9 instructions for 8.  The surplus 24 * sum_k x[m][k] is formed by one more
-//     MFMA against ones and taken off each group's sum.  The larger partial sums triple the fp32
-//     rounding error, from 3e-7 of the result to 1e-6, which a bf16 result does not show and an fp32 one does.
+//     MFMA against ones and taken off each group's sum.  The larger partial sums raise the fp32 rounding error
+//     from 2e-7 of the result to 1e-6, which a bf16 result does not show and an fp32 one does.
 //   - an activation is a sum of NP bf16 pieces (the top 16 bits, then the top 16 bits of the rest, ...):
 //     one piece is exact for bf16 rows, two keep 16 bits for rotated or fp32 rows with a bf16 result
-//     (2^-16 against the result's own 2^-9), three keep all 24 bits for fp32 results.
+//     (2^-16 against the result's own 2^-8), three keep all 24 bits for fp32 results.
 // A lane's 16-byte load holds 32 codes of one channel, and code i of dword j is contracted in MFMA j;
 // the order of k inside the sum is free, so activations are read to match: lane (row r, quarter c)
 // takes k = 32 c + 8 j + i of the 128-code window.
 //
-// A block takes 16 NT channels; its waves take the 128-code windows in turn and their sums are
-// added over LDS.
+// The eight waves of a block take a run of windows each, and their sums are added over LDS.  The channels of a
+// block go by the layer's width, so that one round of blocks fills the 256 CUs (us, one row of bf16):
+//   K = 4096, N = 4096: 16 channels 4.9, 32 6.8, 64 10.2;   N = 8192: 8.1, 7.4, 10.5;   K = 8192, N = 16384: 22.2, 17.6, 18.6
+//   and with 16 rows 26.2, 20.4, 19.8.  Fewer channels than 16 (narrow layers, K >= 2048): N = 1000, K = 4096, 16 rows, 16
+//   channels 5.8, 4 channels 5.3; fp32, one rotated row 8.3 and 7.4.
+// Rows are rotated by every block for itself, or by a kernel before (us, N = 1024): K = 1024, one row 4.5 and 5.9, 12 rows
+// 6.0 and 6.4, 16 rows 6.8 and 6.5; K = 4096, one row 6.2 and 9.5, 5 rows 9.0 and 9.6, 6 rows 9.7 and 9.1.
 #include <hip/hip_bf16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -46,7 +55,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 16;     // activation rows of a block (the MFMA's M)
 constexpr int kWindow = 128;  // codes of a window: one 16-byte load by each quarter of a wave
 
-// Variants by size (see the rules' measurements below).
+// Variants by size (measured above).
 constexpr int kNarrow = 16 * 256;  // channels that one block of 16 on every CU takes
 constexpr int kFused1024 = 12, kFused4096 = 5;  // rows up to which every block rotates them by itself
 
@@ -434,7 +443,8 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
       if constexpr (K != 0) {
 #pragma unroll
         for (int p = 0; p < NP; ++p)
-          xf[j][p] = *reinterpret_cast<const bf16x8*>(split_rows + (row * NP + p) * kPieceRow + win * kWindow + 32 * c + 8 * j);
+          xf[j][p] = *reinterpret_cast<const bf16x8*>(split_rows + (row * NP + p) * kPieceRow + win * kWindow + 32 * c +
+                                                      8 * j);
       } else {
         Eight<X> e;
         load_eight(stage + row * kStageRow + 32 * c + 8 * j, e);
@@ -591,9 +601,10 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
 
 template <typename X, int NP, bool EXACT, int SRC>
 hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
+  // The fewest channels a block with which one round of blocks holds the layer, 64 at most.
   if (a.N > 2 * kNarrow) return launch_kernel<X, NP, EXACT, 4, 1, SRC>(a, st);
   if (a.N > kNarrow) return launch_kernel<X, NP, EXACT, 2, 1, SRC>(a, st);
-  if constexpr (SRC != kRot1024) {  // with 8 windows, one for each wave
+  if constexpr (SRC != kRot1024) {  // K = 1024 has 8 windows, one for each wave
     if (a.K >= 4 * kWaves * kWindow && a.N <= kNarrow / 4) return launch_kernel<X, NP, EXACT, 1, 4, SRC>(a, st);
     if (a.K >= 2 * kWaves * kWindow && a.N <= kNarrow / 2) return launch_kernel<X, NP, EXACT, 1, 2, SRC>(a, st);
   }
