@@ -26,13 +26,16 @@
 // second product is D / 16 fp32 multiply-adds a token.
 // The next unit's keys are loaded as soon as this one's scores are formed, its values as soon as this one's sum is.
 //
-// The tokens of all sequences together are cut into parts of equal size, one round of blocks (kFewBlocks), or more where
-// each part still has kLongPart tokens; a second kernel joins a sequence's parts by their maxima and sums.  Measured
-// with 768, 1024 and 1536 blocks: ragged batch 61, 61, 59 us, long int8 49, 56, 56 (512 blocks: 71 and 58 where 768 took 64 and 54);
-// kLongPart of 768, 1536 and 3072 tokens: long int8 60, 54, 54, large batch 279, 278, 293.
+// The tokens of all sequences together are cut into parts of equal size, one round of the blocks that the chip holds at once,
+// or more where each part still has kLongPart tokens; a second kernel joins a sequence's parts by their maxima and
+// sums.  Measured with one, two and three rounds: ragged batch 60, 58, 61 us, long int8 48, 55, 59, 4 sequences up to
+// 16384 in fp32 41, 42, 45, 64 of 1374 66, 83, 73; with 768 blocks whatever the kernel 61, 49, 45, 66.  kLongPart of 768, 1536
+// and 3072 tokens: long int8 60, 54, 54, large batch 279, 278, 293.
 #include <hip/hip_bf16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "qv_decode_internal.h"
 
@@ -47,6 +50,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 4;  // of a block
 constexpr int kTile = 16;
+constexpr int kCUs = 256, kMaxResident = 8;
+static_assert(kCUs * kMaxResident <= kManyBlocks, "a round of blocks");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;  // finite, so that differences of maxima are never inf - inf
 
@@ -558,6 +563,14 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
   for (int first = 0; first < parts; first += 64) {
     const int p = first + lane, n = parts - first < 64 ? parts - first : 64;
     const float pm = p < parts ? ml[2 * p * step] : kLowest, pl = p < parts ? ml[2 * p * step + 1] : 0.0f;
+    float part_o[64 / kJoinWaves][kPer];  // on their way while the weights are formed
+#pragma unroll
+    for (int i = 0; i < 64 / kJoinWaves; ++i) {
+      const int q = i * kJoinWaves + wave;
+      if (q >= n) break;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) part_o[i][e] = val[(first + q) * step * D + e];
+    }
     float top = fmaxf(m, pm);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
@@ -566,11 +579,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
     l = l * shrink + weight * pl;  // of this lane's parts
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] *= shrink;
-#pragma unroll 8
-    for (int q = wave; q < n; q += kJoinWaves) {
+#pragma unroll
+    for (int i = 0; i < 64 / kJoinWaves; ++i) {
+      const int q = i * kJoinWaves + wave;
+      if (q >= n) break;
       const float w = bits_float(__builtin_amdgcn_readlane(float_bits(weight), q));
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] += w * val[(first + q) * step * D + i];
+      for (int e = 0; e < kPer; ++e) o[e] += w * part_o[i][e];
     }
   }
 #pragma unroll
@@ -587,12 +602,24 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
 }
 
 template <int D, typename X, bool INT8>
-hipError_t launch(const Args& a, bool split, hipStream_t st) {
+hipError_t launch(Args a, bool split, hipStream_t st) {
+  void (*const kernel)(Args) =
+      a.share == 1 ? attention_kernel<D, X, INT8, true, kWaves> : attention_kernel<D, X, INT8, false, kWaves>;
+  static std::atomic<int> resident_blocks[2];  // on a CU, by kernel; 0: not asked for yet; every device is alike
+  std::atomic<int>& resident = resident_blocks[a.share == 1];
+  int n = resident.load(std::memory_order_relaxed);
+  if (n == 0) {
+    const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 64 * kWaves, 0);
+    if (e != hipSuccess) return e;
+    n = n < 1 ? 1 : (n > kMaxResident ? kMaxResident : n);
+    resident.store(n, std::memory_order_relaxed);
+  }
+  // One round of blocks, less half a part a sequence, since the last part of each is half full on average.
+  const int64_t each = (int64_t)a.heads * a.q_tiles, round = (int64_t)n * kCUs / each;
+  a.few = round - a.B / 2 > round / 2 ? round - a.B / 2 : round / 2;
+  if (a.few < 1) a.few = 1;
   const unsigned blocks = a.parts * a.heads * a.q_tiles;
-  if (a.share == 1)
-    attention_kernel<D, X, INT8, true, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
-  else
-    attention_kernel<D, X, INT8, false, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
+  kernel<<<blocks, 64 * kWaves, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !split) return e;
   join_kernel<D, X><<<a.B * a.q_heads, 64 * kJoinWaves, 0, st>>>(a);
@@ -629,7 +656,6 @@ hipError_t launch_paged_attention(const AttentionArgs& in, hipStream_t st) {
   a.share = (uint32_t)(in.q_heads / c.heads);
   a.q_tiles = (a.share + kTile - 1) / kTile;
   const AttentionParts parts = paged_attention_parts(in.B, in.q_heads, c.heads, a.capacity);
-  a.few = parts.few;
   a.many = parts.many;
   a.few_tiles = (in.max_pages * c.page_size + kTile) / kTile * in.B < (int64_t{1} << 31) - kManyBlocks;
   a.parts = (uint32_t)parts.most;

@@ -45,21 +45,20 @@ struct AttentionArgs {
 };
 hipError_t launch_paged_attention(const AttentionArgs& a, hipStream_t st);
 
-// How the batch's tokens are cut into parts of equal size.  `few` parts of all sequences together are one round of
-// blocks on the chip, `many` five; each sequence adds at most one part that is not full, and none has more
-// than its capacity holds.  Each part keeps head_dim + 2 floats for every query head.
+// How the batch's tokens are cut into parts of equal size: at most `many` parts of all sequences together, and one
+// more of each that is not full; no sequence has more than its capacity holds.  Each part keeps head_dim + 2 floats
+// for every query head.
 constexpr int64_t kQueriesPerBlock = 16;    // query heads of one cache head that a block takes
 constexpr int64_t kMinTokensPerPart = 128;  // a unit of work for each wave of a block
 constexpr int64_t kLongPart = 1536;         // tokens from which a block's start no longer counts
-constexpr int64_t kFewBlocks = 768, kManyBlocks = 4096;
+constexpr int64_t kManyBlocks = 4096;       // no less than a round of them
 struct AttentionParts {
-  int64_t few, many, most;
+  int64_t many, most;
   bool split;  // whether a sequence can have more than one
 };
 inline AttentionParts paged_attention_parts(int64_t B, int64_t q_heads, int64_t heads, int64_t capacity) {
   const int64_t each = heads * ((q_heads / heads + kQueriesPerBlock - 1) / kQueriesPerBlock);  // blocks of a part
   AttentionParts p;
-  p.few = (kFewBlocks + each - 1) / each;
   p.many = (kManyBlocks + each - 1) / each;
   p.split = capacity > kMinTokensPerPart;
   const int64_t full = (capacity + kMinTokensPerPart - 1) / kMinTokensPerPart;
