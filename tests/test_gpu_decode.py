@@ -732,3 +732,30 @@ def test_stream_example(dev):
     spec.loader.exec_module(m)
     block, out = m.main(["--frames", "1", "--sequences", "2", "--tokens", "5"])
     assert block.lens.tolist() == [1374 + 6] * 2 and out.shape == (2, 1024)
+
+
+def test_library_refusals_reach_python(qv, dev):
+    """What only the library checks comes back as QVError with its status, and nothing is written."""
+    X, Wq, ws = torch.ones((2, 256), device=dev), torch.zeros((8, 128), dtype=torch.uint8, device=dev), torch.ones((8, 2), device=dev)
+    Y = torch.full((2, 8), 5.0, device=dev)
+    for match, status, call in (
+            ("DTYPE", 5, lambda: qv.qv_w4a16_gemv(X, Wq, ws, 128, None, Y, 7)),
+            ("DTYPE", 5, lambda: qv.qv_w4a16_gemv(X, Wq, ws, 128, None, Y, 1 << 32)),
+            ("UNSUPPORTED", 3, lambda: qv.qv_w4a16_gemv(X, Wq, torch.ones((8, 4), device=dev), 64, None, Y)),
+            ("UNSUPPORTED", 3, lambda: qv.qv_w4a16_linear(X, None, Wq, ws, 128, None, Y,
+                                                          torch.empty(2048, dtype=torch.uint8, device=dev))),
+            ("ALIGN", 4, lambda: qv.qv_w4a16_gemv(torch.ones(513, device=dev)[1:].view(2, 256), Wq, ws, 128, None, Y))):
+        with pytest.raises(qv.QVError, match=match) as e:
+            call()
+        assert e.value.status == status
+    c = make_cache(qv, dev, 2, 2, 16, 64, "bf16", 0)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+    Q = torch.ones((1, 2, 64), device=dev)
+    work = torch.empty(1024, dtype=torch.uint8, device=dev)
+    with pytest.raises(qv.QVError, match="ALIGN"):
+        qv.qv_paged_attention(Q, c, i(1, 2), i(1), torch.empty_like(Q), work[16:])
+    odd = torch.zeros((2, 2, 24, 64), dtype=torch.bfloat16, device=dev)
+    with pytest.raises(qv.QVError, match="UNSUPPORTED"):
+        qv.qv_kv_append(qv.QVKVCache(odd, odd), i(1, 2), i(1), i(1), Q, Q)
+    torch.cuda.synchronize()
+    assert bool((Y == 5.0).all())
