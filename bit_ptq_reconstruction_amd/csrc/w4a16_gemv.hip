@@ -31,6 +31,8 @@
 //   K = 4096, N = 4096: 16 channels 4.9, 32 6.8, 64 10.2;   N = 8192: 8.1, 7.4, 10.5;   K = 8192, N = 16384: 22.2, 17.6, 18.6
 //   and with 16 rows 26.2, 20.4, 19.8.  Fewer channels than 16 (narrow layers, K >= 2048): N = 1000, K = 4096, 16 rows, 16
 //   channels 5.8, 4 channels 5.3; fp32, one rotated row 8.3 and 7.4.
+// Rows beyond 16 count as blocks in that; where 16 to a block would take several rounds, bf16 rows go 32 to a block, which
+// then unpacks each code for both halves: 32 rows x 4096 x 16384 in 22.8 and 15.8 us, 4096 x 4000 in 9.8 and 8.3.
 // Rows are rotated by every block for itself, or by a kernel before (us, N = 1024): K = 1024, one row 4.5 and 5.9, 12 rows
 // 6.0 and 6.4, 16 rows 6.8 and 6.5; K = 4096, one row 6.2 and 9.5, 5 rows 9.0 and 9.6, 6 rows 9.7 and 9.1.
 #include <hip/hip_bf16.h>
@@ -52,11 +54,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr int kRows = 16;     // activation rows of a block (the MFMA's M)
+constexpr int kRows = 16;     // activation rows of a tile (the MFMA's M)
 constexpr int kWindow = 128;  // codes of a window: one 16-byte load by each quarter of a wave
 
 // Variants by size (measured above).
-constexpr int kNarrow = 16 * 256;  // channels that one block of 16 on every CU takes
+constexpr int64_t kCUs = 256;
 constexpr int kFused1024 = 12, kFused4096 = 5;  // rows up to which every block rotates them by itself
 
 // Rotated rows lie in LDS as floats with 8 floats of padding after every 64, so that the strided reads
@@ -294,7 +296,7 @@ struct Args {
 };
 
 // EXACT: fp32 results, codes converted exactly.
-// NT: tiles of 16 channels of a block.  S: with few channels a tile has 16 / S of them and a load S windows, so that
+// MT: tiles of 16 rows of a block.  NT: tiles of 16 channels.  S: with few channels a tile has 16 / S of them and a load S windows, so that
 // more blocks share the codes.
 // SRC: where a wave's operands of the rows come from.
 enum Source {
@@ -317,9 +319,10 @@ __host__ __device__ constexpr int rotated_rows(int rows) {
   return K == 1024 ? (rows + 3) & ~3 : rows;
 }
 
-template <typename X, int NP, bool EXACT, int NT, int S, int SRC>
+template <typename X, int NP, bool EXACT, int MT, int NT, int S, int SRC>
 __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   static_assert(NT == 1 || S == 1, "few channels or many");
+  static_assert(MT == 1 || (S == 1 && SRC == kStaged), "more than 16 rows come from memory");
   constexpr int kDepth = NT == 1 ? 4 : 2;  // loads in flight of each tile
   constexpr int kChannels = 16 / S;        // of a tile
   constexpr int K = kWidth<SRC>;
@@ -328,8 +331,8 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   const int r = lane & 15, c = lane >> 4;
   const int sub = S == 1 ? 0 : r / kChannels;  // which of S windows this lane loads
   const int n0 = blockIdx.x * (kChannels * NT);
-  const int64_t m0 = (int64_t)blockIdx.y * kRows;
-  const int rows = (int)(a.M - m0 < kRows ? a.M - m0 : kRows);
+  const int64_t m0 = (int64_t)blockIdx.y * (MT * kRows);
+  const int rows = (int)(a.M - m0 < MT * kRows ? a.M - m0 : MT * kRows);
   const int windows = a.K / kWindow, groups = a.K / a.group;
   // Rotation: `kAtOnce` rows side by side, as often as there are rows.
   constexpr int kHadamard = K ? K : 1024;  // unused without a rotation
@@ -390,14 +393,16 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
                    put_pieces<NP>(split_rows + (b * kAtOnce + part) * NP * kPieceRow, kPieceRow, k, x);
                  });
   }
-  const int row = r < rows ? r : rows - 1;
+  int row[MT];
+#pragma unroll
+  for (int u = 0; u < MT; ++u) row[u] = kRows * u + r < rows ? kRows * u + r : rows - 1;
 
   // Staged rows: a wave reads its window of every row in one piece, 16 bytes a lane, and holds the next
   // one while it works; 16 bytes of padding a row keep the 16 rows' fragments in different banks.
   constexpr int kPerLoad = 16 / (int)sizeof(X);      // activations
   constexpr int kLanesPerRow = kWindow / kPerLoad;   // 16 (bf16) or 32 (fp32)
   constexpr int kRowsPerLoad = 64 / kLanesPerRow;
-  constexpr int kLoads = kRows / kRowsPerLoad;
+  constexpr int kLoads = MT * kRows / kRowsPerLoad;
   constexpr int kStageRow = kWindow + kPerLoad;      // activations
   X* const stage = reinterpret_cast<X*>(room) + wave * (rows * kStageRow);
   const int stage_row = lane / kLanesPerRow, stage_k = (lane % kLanesPerRow) * kPerLoad;
@@ -415,16 +420,18 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   }
   if constexpr (K != 0) __syncthreads();
 
-  f32x4 y[NT];
+  f32x4 y[NT][MT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) y[t] = f32x4{0, 0, 0, 0};
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int u = 0; u < MT; ++u) y[t][u] = f32x4{0, 0, 0, 0};
   bf16x8 ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 
-  // The rows' operands of a window, and the sum of its activations.
-  bf16x8 xf[4][NP];
-  f32x4 sum;
+  // The rows' operands of a window, and the sums of its activations.
+  bf16x8 xf[MT][4][NP];
+  f32x4 sum[MT];
   auto take_rows = [&](int win) {
     if constexpr (K == 0) {
 #pragma unroll
@@ -439,38 +446,48 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
       if (win + 1 < end) load_stage(win + 1);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (K != 0) {
+    for (int u = 0; u < MT; ++u) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-          xf[j][p] = *reinterpret_cast<const bf16x8*>(split_rows + (row * NP + p) * kPieceRow + win * kWindow + 32 * c +
-                                                      8 * j);
-      } else {
-        Eight<X> e;
-        load_eight(stage + row * kStageRow + 32 * c + 8 * j, e);
-        pieces<NP>(e, xf[j]);
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (K != 0) {
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            xf[u][j][p] = *reinterpret_cast<const bf16x8*>(split_rows + (row[u] * NP + p) * kPieceRow + win * kWindow +
+                                                           32 * c + 8 * j);
+        } else {
+          Eight<X> e;
+          load_eight(stage + row[u] * kStageRow + 32 * c + 8 * j, e);
+          pieces<NP>(e, xf[u][j]);
+        }
       }
     }
     if constexpr (K == 0) __builtin_amdgcn_wave_barrier();
-    sum = f32x4{0, 0, 0, 0};
-    if constexpr (!EXACT) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+    for (int u = 0; u < MT; ++u) {
+      sum[u] = f32x4{0, 0, 0, 0};
+      if constexpr (!EXACT) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], ones, sum, 0, 0, 0);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            sum[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][j][p], ones, sum[u], 0, 0, 0);
+      }
     }
   };
-  auto product = [&](const u32x4& codes) {
-    f32x4 acc = {0, 0, 0, 0};
+  auto product = [&](const u32x4& codes, f32x4 (&acc)[MT]) {
+#pragma unroll
+    for (int u = 0; u < MT; ++u) acc[u] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bf16x8 wf = EXACT ? widen_exact(codes[j]) : widen(codes[j]);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], wf, acc, 0, 0, 0);
+      for (int u = 0; u < MT; ++u)
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][j][p], wf, acc[u], 0, 0, 0);
     }
-    return acc;
   };
-  auto add = [&](f32x4& to, float f, const f32x4& acc) {
+  auto add = [&](f32x4& to, float f, const f32x4& acc, const f32x4& sum) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] += EXACT ? 16.0f * f * acc[i] : f * (acc[i] - 24.0f * sum[i]);
   };
@@ -484,18 +501,18 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
     for (int d = 0; d < 4; ++d) {
       const int win = first + d * S;
       if (win >= end) break;
-      f32x4 acc[NT];
+      f32x4 acc[NT][MT];
       if constexpr (S == 1) {
         take_rows(win);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] = product(w[d % kDepth][t]);
+        for (int t = 0; t < NT; ++t) product(w[d % kDepth][t], acc[t]);
       } else {
         // A load's columns belong to S windows: each window's product is taken with all of them and its own are kept.
         bf16x8 wf[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) wf[j] = EXACT ? widen_exact(w[d][0][j]) : widen(w[d][0][j]);
         f32x4 own = {0, 0, 0, 0};
-        acc[0] = own;
+        acc[0][0] = own;
 #pragma unroll
         for (int u = 0; u < S; ++u) {
           if (win + u >= end) break;
@@ -504,37 +521,44 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int p = 0; p < NP; ++p) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][p], wf[j], x, 0, 0, 0);
+            for (int p = 0; p < NP; ++p) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[0][j][p], wf[j], x, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            acc[0][i] = sub == u ? x[i] : acc[0][i];
-            own[i] = sub == u ? sum[i] : own[i];
+            acc[0][0][i] = sub == u ? x[i] : acc[0][0][i];
+            own[i] = sub == u ? sum[0][i] : own[i];
           }
         }
-        sum = own;
+        sum[0] = own;
       }
       if (win + kDepth * S < end) load_codes(d % kDepth, win + kDepth * S);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) add(y[t], __shfl(sc[t], r + 16 * d), acc[t]);
+      for (int t = 0; t < NT; ++t) {
+        const float f = __shfl(sc[t], r + 16 * d);
+#pragma unroll
+        for (int u = 0; u < MT; ++u) add(y[t][u], f, acc[t][u], sum[u]);
+      }
     }
   }
 
-  // Element (m, n) of tile t at [wave][t][m][n].
+  // Element (m, n) of channel tile t and row tile u at [wave][t][u][m][n].
   if constexpr (K == 0) __syncthreads();  // the sums take the staging regions' place
   float* const red = reinterpret_cast<float*>(room + (K ? rotated_rows<K>(rows) * rotated_bytes<K, NP>() : 0));
+  constexpr int kTiles = NT * MT;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[(wave * NT + t) * 256 + (4 * c + i) * 16 + r] = y[t][i];
+    for (int u = 0; u < MT; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[((wave * NT + t) * MT + u) * 256 + (4 * c + i) * 16 + r] = y[t][u][i];
   __syncthreads();
-  for (int idx = threadIdx.x; idx < 256 * NT; idx += kThreads) {
-    const int t = idx >> 8, m = (idx >> 4) & 15, n = n0 + 16 * t + (idx & 15);
+  for (int idx = threadIdx.x; idx < 256 * kTiles; idx += kThreads) {
+    const int t = idx / (256 * MT), m = (idx >> 4) & (16 * MT - 1), n = n0 + 16 * t + (idx & 15);
     if (m >= rows || n >= a.N || (S > 1 && (idx & 15) >= kChannels)) continue;
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < kWaves; ++k)
 #pragma unroll
-      for (int u = 0; u < S; ++u) v += red[k * NT * 256 + idx + u * kChannels];
+      for (int u = 0; u < S; ++u) v += red[k * kTiles * 256 + idx + u * kChannels];
     if (a.bias) v += a.bias[n];
     if (a.gelu) v = gelu(v);
     const int64_t at = (m0 + m) * a.ldy + n;
@@ -558,13 +582,13 @@ __global__ __launch_bounds__(K / 8) void rotate_rows_kernel(const X* __restrict_
   rotation.run(reinterpret_cast<float*>(row4), 0, 1, t, [&](int, int k, float v) { to[k] = v; });
 }
 
-template <typename X, int NP, bool EXACT, int NT, int S, int SRC>
+template <typename X, int NP, bool EXACT, int MT, int NT, int S, int SRC>
 hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
   constexpr int K = kWidth<SRC>;
   constexpr int kBlock = 16 / S * NT;  // channels
   const unsigned gx = (unsigned)((a.N + kBlock - 1) / kBlock);
-  const int rows = (int)(a.M < kRows ? a.M : kRows);
-  size_t bytes = (size_t)kWaves * NT * 256 * 4;
+  const int rows = (int)(a.M < MT * kRows ? a.M : MT * kRows);
+  size_t bytes = (size_t)kWaves * NT * MT * 256 * 4;
   if (K) {
     bytes += (size_t)rotated_rows<K>(rows) * rotated_bytes<K, NP>();
   } else {
@@ -578,21 +602,21 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
     if (e != hipSuccess) return e;
     const uint64_t bit = uint64_t{1} << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&w4a16_kernel<X, NP, EXACT, NT, S, SRC>),
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&w4a16_kernel<X, NP, EXACT, MT, NT, S, SRC>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
       if (e != hipSuccess) return e;
       raised.fetch_or(bit, std::memory_order_relaxed);
     }
   }
   // grid.y holds 65535 blocks: longer runs go in several launches
-  const int64_t step = (int64_t)65535 * kRows;
+  const int64_t step = (int64_t)65535 * MT * kRows;
   for (int64_t m = 0; m < a.M; m += step) {
     Args<X> b = a;
     b.x += m * a.ldx;
     b.M = a.M - m < step ? a.M - m : step;
     b.y = static_cast<char*>(a.y) + m * a.ldy * (a.y_bf16 ? 2 : 4);
-    w4a16_kernel<X, NP, EXACT, NT, S, SRC>
-        <<<dim3(gx, (unsigned)((b.M + kRows - 1) / kRows)), kThreads, bytes, st>>>(b);
+    w4a16_kernel<X, NP, EXACT, MT, NT, S, SRC>
+        <<<dim3(gx, (unsigned)((b.M + MT * kRows - 1) / (MT * kRows))), kThreads, bytes, st>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -602,13 +626,24 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
 template <typename X, int NP, bool EXACT, int SRC>
 hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
   // The fewest channels a block with which one round of blocks holds the layer, 64 at most.
-  if (a.N > 2 * kNarrow) return launch_kernel<X, NP, EXACT, 4, 1, SRC>(a, st);
-  if (a.N > kNarrow) return launch_kernel<X, NP, EXACT, 2, 1, SRC>(a, st);
-  if constexpr (SRC != kRot1024) {  // K = 1024 has 8 windows, one for each wave
-    if (a.K >= 4 * kWaves * kWindow && a.N <= kNarrow / 4) return launch_kernel<X, NP, EXACT, 1, 4, SRC>(a, st);
-    if (a.K >= 2 * kWaves * kWindow && a.N <= kNarrow / 2) return launch_kernel<X, NP, EXACT, 1, 2, SRC>(a, st);
+  auto fits = [&](int rows, int channels) {
+    return ((a.M + rows - 1) / rows) * ((a.N + channels - 1) / channels) <= kCUs;
+  };
+  // Rows of one piece (more do not fit the registers) go 32 to a block where 16 would take several rounds.
+  if constexpr (SRC == kStaged && NP == 1) {
+    if (a.M > kRows && !fits(kRows, 16)) {
+      if (fits(2 * kRows, 16)) return launch_kernel<X, NP, EXACT, 2, 1, 1, SRC>(a, st);
+      if (fits(2 * kRows, 32)) return launch_kernel<X, NP, EXACT, 2, 2, 1, SRC>(a, st);
+      return launch_kernel<X, NP, EXACT, 2, 4, 1, SRC>(a, st);
+    }
   }
-  return launch_kernel<X, NP, EXACT, 1, 1, SRC>(a, st);
+  if (!fits(kRows, 32)) return launch_kernel<X, NP, EXACT, 1, 4, 1, SRC>(a, st);
+  if (!fits(kRows, 16)) return launch_kernel<X, NP, EXACT, 1, 2, 1, SRC>(a, st);
+  if constexpr (SRC != kRot1024) {  // K = 1024 has 8 windows, one for each wave
+    if (a.K >= 4 * kWaves * kWindow && fits(kRows, 4)) return launch_kernel<X, NP, EXACT, 1, 1, 4, SRC>(a, st);
+    if (a.K >= 2 * kWaves * kWindow && fits(kRows, 8)) return launch_kernel<X, NP, EXACT, 1, 1, 2, SRC>(a, st);
+  }
+  return launch_kernel<X, NP, EXACT, 1, 1, 1, SRC>(a, st);
 }
 
 // Pieces by the types: rows that are bf16 are one piece; others two or, for fp32 results, three.

@@ -101,6 +101,10 @@ GEMV = [  # M, K, N, group, x, y, bias, gelu, padding of the rows of X and Y
     (16, 8192, 6000, 128, "bf16", "bf16", False, False, 0, 0),
     (1, 8192, 20001, 8192, "fp32", "bf16", False, False, 0, 0),
     (64, 256, 333, 128, "fp32", "bf16", False, False, 0, 0),
+    (20, 1024, 4000, 128, "bf16", "bf16", True, True, 8, 3),
+    (29, 384, 4100, 384, "bf16", "fp32", True, False, 0, 1),
+    (70, 256, 9000, 128, "bf16", "bf16", False, False, 0, 0),
+    (33, 2048, 2100, 512, "fp32", "bf16", True, False, 4, 0),
 ]
 
 
