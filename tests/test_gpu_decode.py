@@ -763,3 +763,21 @@ def test_library_refusals_reach_python(qv, dev):
         qv.qv_kv_append(qv.QVKVCache(odd, odd), i(1, 2), i(1), i(1), Q, Q)
     torch.cuda.synchronize()
     assert bool((Y == 5.0).all())
+
+
+def test_append_int8_near_ties(qv, dev):
+    """Quotients at and next to half-integers, for scales that are no powers of two: codes equal those of the division."""
+    g = gen(31)
+    T = 512
+    scale = 10.0 ** (torch.rand((T, 1, 1), generator=g) * 12 - 6)
+    half = torch.randint(-127, 127, (T, 1, 64), generator=g) + 0.5
+    V = (half * scale).float()
+    V = torch.where(torch.rand(V.shape, generator=g) < 0.5, torch.nextafter(V, torch.full_like(V, float("inf"))), V)
+    V[:, 0, 0] = (127.0 * scale[:, 0, 0]).float()
+    cache = make_cache(qv, dev, T // 16, 1, 16, 64, "int8", 0)
+    i = torch.arange(T, dtype=torch.int32, device=dev)
+    table = torch.arange(T // 16, dtype=torch.int32, device=dev)[None]
+    qv.qv_kv_append(cache, table, torch.zeros_like(i), i, V.to(dev), V.to(dev))
+    codes, scales = codes32(V)
+    assert torch.equal(cache.v_pages.cpu().view(T, 1, 64), codes)
+    assert torch.equal(cache.v_scale.cpu().view(T, 1), scales)
