@@ -296,8 +296,8 @@ struct Args {
 };
 
 // EXACT: fp32 results, codes converted exactly.
-// MT: tiles of 16 rows of a block.  NT: tiles of 16 channels.  S: with few channels a tile has 16 / S of them and a load S windows, so that
-// more blocks share the codes.
+// MT: tiles of 16 rows of a block.  NT: tiles of 16 channels.
+// S: with few channels a tile has 16 / S of them and a load S windows, so that more blocks share the codes.
 // SRC: where a wave's operands of the rows come from.
 enum Source {
   kStaged,            // memory, through an LDS region of the wave's own, so that a row's window is read in one piece
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   constexpr int kChannels = 16 / S;        // of a tile
   constexpr int K = kWidth<SRC>;
   extern __shared__ f32x4 lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int sub = S == 1 ? 0 : r / kChannels;  // which of S windows this lane loads
   const int n0 = blockIdx.x * (kChannels * NT);
