@@ -626,8 +626,8 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
 template <typename X, int NP, bool EXACT, int SRC>
 hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
   // The fewest channels a block with which one round of blocks holds the layer, 64 at most.
-  auto fits = [&](int rows, int channels) {
-    return ((a.M + rows - 1) / rows) * ((a.N + channels - 1) / channels) <= kCUs;
+  auto fits = [&](int rows, int channels, int blocks_a_cu = 1) {
+    return ((a.M + rows - 1) / rows) * ((a.N + channels - 1) / channels) <= blocks_a_cu * kCUs;
   };
   // Rows of one piece (more do not fit the registers) go 32 to a block where 16 would take several rounds.
   if constexpr (SRC == kStaged && NP == 1) {
@@ -637,7 +637,11 @@ hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
       return launch_kernel<X, NP, EXACT, 2, 4, 1, SRC>(a, st);
     }
   }
-  if (!fits(kRows, 32)) return launch_kernel<X, NP, EXACT, 1, 4, 1, SRC>(a, st);
+  // Two blocks of 32 channels share a CU where their registers (bf16 rows) and LDS (rotated rows) allow it; with more than
+  // a few rows, reading the rows twice costs more than that gives: K = 4096, N = 16384, rows read and 1, 8, 16 of them 10.6, 11.4,
+  // 12.8 us (64 channels: 11.6, 12.0, 12.9), rotated and 1, 4 of them 13.0, 21.0 us (14.5, 16.3).
+  const bool two = sizeof(X) == 2 && a.M <= (SRC == kStaged ? 8 : 3);
+  if (!fits(kRows, 32, two ? 2 : 1)) return launch_kernel<X, NP, EXACT, 1, 4, 1, SRC>(a, st);
   if (!fits(kRows, 16)) return launch_kernel<X, NP, EXACT, 1, 2, 1, SRC>(a, st);
   if constexpr (SRC != kRot1024) {  // K = 1024 has 8 windows, one for each wave
     if (a.K >= 4 * kWaves * kWindow && fits(kRows, 4)) return launch_kernel<X, NP, EXACT, 1, 1, 4, SRC>(a, st);

@@ -105,6 +105,8 @@ GEMV = [  # M, K, N, group, x, y, bias, gelu, padding of the rows of X and Y
     (29, 384, 4100, 384, "bf16", "fp32", True, False, 0, 1),
     (70, 256, 9000, 128, "bf16", "bf16", False, False, 0, 0),
     (33, 2048, 2100, 512, "fp32", "bf16", True, False, 4, 0),
+    (5, 1152, 9001, 128, "bf16", "fp32", True, False, 0, 0),
+    (9, 1024, 10000, 256, "bf16", "bf16", False, False, 0, 0),
 ]
 
 
@@ -132,6 +134,8 @@ def test_gemv(qv, dev, M, K, N, group, xt, yt, bias, gelu, padx, pady):
     (4, 1024, 65, 512, "bf16", "bf16", True, False, 0), (5, 1024, 129, 256, "bf16", "bf16", False, True, 0),
     (7, 4096, 50, 4096, "fp32", "bf16", True, False, 0), (13, 1024, 4099, 1024, "fp32", "fp32", True, True, 0),
     (16, 4096, 300, 128, "bf16", "bf16", True, False, 0), (35, 1024, 64, 128, "bf16", "bf16", True, False, 0),
+    (2, 1024, 9000, 128, "bf16", "bf16", True, False, 0), (3, 4096, 9000, 512, "bf16", "fp32", True, False, 0),
+    (5, 4096, 5000, 256, "fp32", "fp32", False, False, 4), (12, 1024, 4500, 128, "bf16", "bf16", True, False, 0),
 ])
 def test_linear(qv, dev, M, K, N, group, xt, yt, smooth, gelu, padx):
     g = gen(M * 7919 + K + N)
