@@ -4,9 +4,9 @@
 //   O[b][i] = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q_i . k_t - m),  m the running maximum
 //
 // One pass over the keys and values, which is all there is to move: the kernel is bound by memory.  48 sequences of up to
-// 16384 tokens (8 heads of 128, 32 queries, 1.6 GB) take 271 us, 6.0 TB/s (a copy runs at 5.0; the matrix cores are busy for 6 %
-// and the vector ALU for 13 % of the time); two of 99991 tokens in int8 (211 MB) take 49-51 us, 4.2 TB/s (vector ALU
-// 41 %, for the conversions).  One frame of 1374 tokens (5.6 MB) takes 7.9 us: 5.0 for the parts' chain of loads (lengths,
+// 16384 tokens (8 heads of 128, 32 queries, 1.6 GB) take 270 us, 6.0 TB/s (a copy runs at 5.0; the matrix cores are busy for 6 %
+// and the vector ALU for 13 % of the time); two of 99991 tokens in int8 (211 MB) take 47-48 us, 4.4 TB/s (vector ALU
+// 43 %, for the conversions).  One frame of 1374 tokens (5.6 MB) takes 7.9 us: 5.0 for the parts' chain of loads (lengths,
 // page table, keys) and 2.9 for the join.
 //
 // A wave takes two tiles of 16 tokens at a time and the up to 16 query heads that share a cache head, and nothing leaves its
@@ -540,13 +540,12 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
   }
 }
 
-// Parts joined: one block to a query head.  Every wave weighs all parts by itself (lane p of 64 at a time), adds every
-// kJoinWaves-th of them, several loads in flight, and the waves' sums meet once in LDS.
-constexpr int kJoinWaves = 8;
-template <int D, typename X>
-__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
+// Parts joined: one block of W waves to a query head.  Every wave weighs all parts by itself (lane p of 64 at a time), adds
+// every W-th of them, and the waves' sums meet once in LDS.
+template <int D, typename X, int W>
+__global__ __launch_bounds__(64 * W) void join_kernel(Args a) {
   constexpr int kPer = D / 64;  // channels of a lane
-  __shared__ float sums[kJoinWaves][D];
+  __shared__ float sums[W][D];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t b = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
   const Part part = find_part<false>(a, (int)b);
@@ -563,10 +562,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
   for (int first = 0; first < parts; first += 64) {
     const int p = first + lane, n = parts - first < 64 ? parts - first : 64;
     const float pm = p < parts ? ml[2 * p * step] : kLowest, pl = p < parts ? ml[2 * p * step + 1] : 0.0f;
-    float part_o[64 / kJoinWaves][kPer];  // on their way while the weights are formed
+    float part_o[64 / W][kPer];  // on their way while the weights are formed
 #pragma unroll
-    for (int i = 0; i < 64 / kJoinWaves; ++i) {
-      const int q = i * kJoinWaves + wave;
+    for (int i = 0; i < 64 / W; ++i) {
+      const int q = i * W + wave;
       if (q >= n) break;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) part_o[i][e] = val[(first + q) * step * D + e];
@@ -580,8 +579,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] *= shrink;
 #pragma unroll
-    for (int i = 0; i < 64 / kJoinWaves; ++i) {
-      const int q = i * kJoinWaves + wave;
+    for (int i = 0; i < 64 / W; ++i) {
+      const int q = i * W + wave;
       if (q >= n) break;
       const float w = bits_float(__builtin_amdgcn_readlane(float_bits(weight), q));
 #pragma unroll
@@ -593,10 +592,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Args a) {
 #pragma unroll
   for (int i = 0; i < kPer; ++i) sums[wave][kPer * lane + i] = o[i];
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += 64 * kJoinWaves) {
+  for (int d = threadIdx.x; d < D; d += 64 * W) {
     float x = sums[0][d];
 #pragma unroll
-    for (int w = 1; w < kJoinWaves; ++w) x += sums[w][d];
+    for (int w = 1; w < W; ++w) x += sums[w][d];
     store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, l > 0.0f ? x / l : 0.0f);
   }
 }
@@ -622,7 +621,12 @@ hipError_t launch(Args a, bool split, hipStream_t st) {
   kernel<<<blocks, 64 * kWaves, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !split) return e;
-  join_kernel<D, X><<<a.B * a.q_heads, 64 * kJoinWaves, 0, st>>>(a);
+  // Many heads fill the chip with two waves each; few heads have many parts, which eight waves read at once (us, two and
+  // eight waves: ragged batch 60.1 and 60.9, large batch 270.4 and 272.4, long int8 60.1 and 49.9).
+  if (a.B * a.q_heads > 2 * kCUs)
+    join_kernel<D, X, 2><<<a.B * a.q_heads, 128, 0, st>>>(a);
+  else
+    join_kernel<D, X, 8><<<a.B * a.q_heads, 512, 0, st>>>(a);
   return hipGetLastError();
 }
 
