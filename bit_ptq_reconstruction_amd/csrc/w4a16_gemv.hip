@@ -13,12 +13,10 @@
 // Products run on the matrix cores, 16 rows x 16 channels x 32 codes at a time, whatever M is: one
 // v_mfma_f32_16x16x32_bf16 replaces 512 multiply-adds for 16 cycles, and the vector ALU is left with
 // the unpacking.  Both operands are exact in bf16:
-//   - with fp32 results a code is converted by itself (v_cvt_off_f32_i4 gives q / 16, and the upper halves
-//     of two are packed: 19 instructions for 8 codes).
-//   - with bf16 results a code q becomes 24 + q in [16, 31], i.e. the bits 0x4180 | (q + 8) << 3: one shift
-//     and one and-or for two codes, 9 instructions for 8.  The surplus 24 * sum_k x[m][k] is formed by one more
-//     MFMA against ones and taken off each group's sum.  The larger partial sums raise the fp32 rounding error
-//     from 2e-7 of the result to 1e-6, which a bf16 result does not show and an fp32 one does.
+//   - a code is converted by itself (v_cvt_off_f32_i4 gives q / 16, and the upper halves of two are packed: 13
+//     instructions for 8 codes).  24 + q, whose bits are one shift and one and-or for two codes (9 for 8), with
+//     24 sum_k x[m][k] taken off each group's sum, would round every sum at the size of 24 |x|: a large activation against
+//     a code of zero has to add nothing.
 //   - an activation is a sum of NP bf16 pieces (the top 16 bits, then the top 16 bits of the rest, ...):
 //     one piece is exact for bf16 rows, two keep 16 bits for rotated or fp32 rows with a bf16 result
 //     (2^-16 against the result's own 2^-8), three keep all 24 bits for fp32 results.
@@ -119,26 +117,29 @@ __device__ __forceinline__ void pieces(const Eight<float>& v, bf16x8 (&f)[NP]) {
   }
 }
 
-// Eight codes -> q / 16 in bf16, exactly, dword s holding codes s and s + 4.
-__device__ __forceinline__ bf16x8 widen_exact(unsigned w) {
-  u32x4 o;
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const float a = __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * s)));
-    const float b = __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * s + 16)));
-    o[s] = __builtin_amdgcn_perm(float_bits(b), float_bits(a), 0x07060302u);
-  }
-  return __builtin_bit_cast(bf16x8, o);
+// The low nibble of byte i of a dword -> q / 16, in one instruction.
+template <int i>
+__device__ __forceinline__ unsigned low_code(unsigned w) {
+  unsigned f;
+  if constexpr (i == 0)
+    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(w));
+  else if constexpr (i == 1)
+    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(w));
+  else if constexpr (i == 2)
+    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(w));
+  else
+    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(w));
+  return f;
 }
 
-// Eight codes -> 24 + q in bf16, dword s holding codes s and s + 4.
+// Eight codes -> q / 16 in bf16, exactly, dword s holding codes s and s + 4.
 __device__ __forceinline__ bf16x8 widen(unsigned w) {
-  const unsigned u = w ^ 0x88888888u;  // q + 8 in each nibble
+  const unsigned odd = w >> 4;  // codes 1, 3, 5, 7 in the low nibbles
   u32x4 o;
-  o[0] = ((u << 3) & 0x00780078u) | 0x41804180u;
-  o[1] = ((u >> 1) & 0x00780078u) | 0x41804180u;
-  o[2] = ((u >> 5) & 0x00780078u) | 0x41804180u;
-  o[3] = ((u >> 9) & 0x00780078u) | 0x41804180u;
+  o[0] = __builtin_amdgcn_perm(low_code<2>(w), low_code<0>(w), 0x07060302u);
+  o[1] = __builtin_amdgcn_perm(low_code<2>(odd), low_code<0>(odd), 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(low_code<3>(w), low_code<1>(w), 0x07060302u);
+  o[3] = __builtin_amdgcn_perm(low_code<3>(odd), low_code<1>(odd), 0x07060302u);
   return __builtin_bit_cast(bf16x8, o);
 }
 
@@ -295,7 +296,6 @@ struct Args {
   int gelu, y_bf16;
 };
 
-// EXACT: fp32 results, codes converted exactly.
 // MT: tiles of 16 rows of a block.  NT: tiles of 16 channels.
 // S: with few channels a tile has 16 / S of them and a load S windows, so that more blocks share the codes.
 // SRC: where a wave's operands of the rows come from.
@@ -319,7 +319,7 @@ __host__ __device__ constexpr int rotated_rows(int rows) {
   return K == 1024 ? (rows + 3) & ~3 : rows;
 }
 
-template <typename X, int NP, bool EXACT, int MT, int NT, int S, int SRC>
+template <typename X, int NP, int MT, int NT, int S, int SRC>
 __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   static_assert(NT == 1 || S == 1, "few channels or many");
   static_assert(MT == 1 || (S == 1 && SRC == kStaged), "more than 16 rows come from memory");
@@ -425,13 +425,9 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int u = 0; u < MT; ++u) y[t][u] = f32x4{0, 0, 0, 0};
-  bf16x8 ones;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 
-  // The rows' operands of a window, and the sums of its activations.
+  // The rows' operands of a window.
   bf16x8 xf[MT][4][NP];
-  f32x4 sum[MT];
   auto take_rows = [&](int win) {
     if constexpr (K == 0) {
 #pragma unroll
@@ -462,24 +458,13 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
       }
     }
     if constexpr (K == 0) __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int u = 0; u < MT; ++u) {
-      sum[u] = f32x4{0, 0, 0, 0};
-      if constexpr (!EXACT) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int p = 0; p < NP; ++p)
-            sum[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][j][p], ones, sum[u], 0, 0, 0);
-      }
-    }
   };
   auto product = [&](const u32x4& codes, f32x4 (&acc)[MT]) {
 #pragma unroll
     for (int u = 0; u < MT; ++u) acc[u] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bf16x8 wf = EXACT ? widen_exact(codes[j]) : widen(codes[j]);
+      const bf16x8 wf = widen(codes[j]);
 #pragma unroll
       for (int u = 0; u < MT; ++u)
 #pragma unroll
@@ -487,9 +472,9 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
           acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][j][p], wf, acc[u], 0, 0, 0);
     }
   };
-  auto add = [&](f32x4& to, float f, const f32x4& acc, const f32x4& sum) {
+  auto add = [&](f32x4& to, float f, const f32x4& acc) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) to[i] += EXACT ? 16.0f * f * acc[i] : f * (acc[i] - 24.0f * sum[i]);
+    for (int i = 0; i < 4; ++i) to[i] += 16.0f * f * acc[i];
   };
 
   for (int first = begin; first < end; first += 4 * S) {
@@ -510,9 +495,8 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
         // A load's columns belong to S windows: each window's product is taken with all of them and its own are kept.
         bf16x8 wf[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wf[j] = EXACT ? widen_exact(w[d][0][j]) : widen(w[d][0][j]);
-        f32x4 own = {0, 0, 0, 0};
-        acc[0][0] = own;
+        for (int j = 0; j < 4; ++j) wf[j] = widen(w[d][0][j]);
+        acc[0][0] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int u = 0; u < S; ++u) {
           if (win + u >= end) break;
@@ -523,19 +507,15 @@ __global__ __launch_bounds__(kThreads) void w4a16_kernel(Args<X> a) {
 #pragma unroll
             for (int p = 0; p < NP; ++p) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[0][j][p], wf[j], x, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[0][0][i] = sub == u ? x[i] : acc[0][0][i];
-            own[i] = sub == u ? sum[0][i] : own[i];
-          }
+          for (int i = 0; i < 4; ++i) acc[0][0][i] = sub == u ? x[i] : acc[0][0][i];
         }
-        sum[0] = own;
       }
       if (win + kDepth * S < end) load_codes(d % kDepth, win + kDepth * S);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float f = __shfl(sc[t], r + 16 * d);
 #pragma unroll
-        for (int u = 0; u < MT; ++u) add(y[t][u], f, acc[t][u], sum[u]);
+        for (int u = 0; u < MT; ++u) add(y[t][u], f, acc[t][u]);
       }
     }
   }
@@ -582,7 +562,7 @@ __global__ __launch_bounds__(K / 8) void rotate_rows_kernel(const X* __restrict_
   rotation.run(reinterpret_cast<float*>(row4), 0, 1, t, [&](int, int k, float v) { to[k] = v; });
 }
 
-template <typename X, int NP, bool EXACT, int MT, int NT, int S, int SRC>
+template <typename X, int NP, int MT, int NT, int S, int SRC>
 hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
   constexpr int K = kWidth<SRC>;
   constexpr int kBlock = 16 / S * NT;  // channels
@@ -602,7 +582,7 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
     if (e != hipSuccess) return e;
     const uint64_t bit = uint64_t{1} << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&w4a16_kernel<X, NP, EXACT, MT, NT, S, SRC>),
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&w4a16_kernel<X, NP, MT, NT, S, SRC>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
       if (e != hipSuccess) return e;
       raised.fetch_or(bit, std::memory_order_relaxed);
@@ -615,7 +595,7 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
     b.x += m * a.ldx;
     b.M = a.M - m < step ? a.M - m : step;
     b.y = static_cast<char*>(a.y) + m * a.ldy * (a.y_bf16 ? 2 : 4);
-    w4a16_kernel<X, NP, EXACT, MT, NT, S, SRC>
+    w4a16_kernel<X, NP, MT, NT, S, SRC>
         <<<dim3(gx, (unsigned)((b.M + MT * kRows - 1) / (MT * kRows))), kThreads, bytes, st>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -623,7 +603,7 @@ hipError_t launch_kernel(const Args<X>& a, hipStream_t st) {
   return hipSuccess;
 }
 
-template <typename X, int NP, bool EXACT, int SRC>
+template <typename X, int NP, int SRC>
 hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
   // The fewest channels a block with which one round of blocks holds the layer, 64 at most.
   auto fits = [&](int rows, int channels, int blocks_a_cu = 1) {
@@ -632,31 +612,31 @@ hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
   // Rows of one piece (more do not fit the registers) go 32 to a block where 16 would take several rounds.
   if constexpr (SRC == kStaged && NP == 1) {
     if (a.M > kRows && !fits(kRows, 16)) {
-      if (fits(2 * kRows, 16)) return launch_kernel<X, NP, EXACT, 2, 1, 1, SRC>(a, st);
-      if (fits(2 * kRows, 32)) return launch_kernel<X, NP, EXACT, 2, 2, 1, SRC>(a, st);
-      return launch_kernel<X, NP, EXACT, 2, 4, 1, SRC>(a, st);
+      if (fits(2 * kRows, 16)) return launch_kernel<X, NP, 2, 1, 1, SRC>(a, st);
+      if (fits(2 * kRows, 32)) return launch_kernel<X, NP, 2, 2, 1, SRC>(a, st);
+      return launch_kernel<X, NP, 2, 4, 1, SRC>(a, st);
     }
   }
   // Two blocks of 32 channels share a CU where their registers (bf16 rows) and LDS (rotated rows) allow it; with more than
   // a few rows, reading the rows twice costs more than that gives: K = 4096, N = 16384, rows read and 1, 8, 16 of them 10.6, 11.4,
   // 12.8 us (64 channels: 11.6, 12.0, 12.9), rotated and 1, 4 of them 13.0, 21.0 us (14.5, 16.3).
   const bool two = sizeof(X) == 2 && a.M <= (SRC == kStaged ? 8 : 3);
-  if (!fits(kRows, 32, two ? 2 : 1)) return launch_kernel<X, NP, EXACT, 1, 4, 1, SRC>(a, st);
-  if (!fits(kRows, 16)) return launch_kernel<X, NP, EXACT, 1, 2, 1, SRC>(a, st);
+  if (!fits(kRows, 32, two ? 2 : 1)) return launch_kernel<X, NP, 1, 4, 1, SRC>(a, st);
+  if (!fits(kRows, 16)) return launch_kernel<X, NP, 1, 2, 1, SRC>(a, st);
   if constexpr (SRC != kRot1024) {  // K = 1024 has 8 windows, one for each wave
-    if (a.K >= 4 * kWaves * kWindow && fits(kRows, 4)) return launch_kernel<X, NP, EXACT, 1, 1, 4, SRC>(a, st);
-    if (a.K >= 2 * kWaves * kWindow && fits(kRows, 8)) return launch_kernel<X, NP, EXACT, 1, 1, 2, SRC>(a, st);
+    if (a.K >= 4 * kWaves * kWindow && fits(kRows, 4)) return launch_kernel<X, NP, 1, 1, 4, SRC>(a, st);
+    if (a.K >= 2 * kWaves * kWindow && fits(kRows, 8)) return launch_kernel<X, NP, 1, 1, 2, SRC>(a, st);
   }
-  return launch_kernel<X, NP, EXACT, 1, 1, 1, SRC>(a, st);
+  return launch_kernel<X, NP, 1, 1, 1, SRC>(a, st);
 }
 
 // Pieces by the types: rows that are bf16 are one piece; others two or, for fp32 results, three.
 template <typename X, int SRC>
 hipError_t by_types(const Args<X>& a, hipStream_t st) {
   if constexpr (sizeof(X) == 2 && kWidth<SRC> == 0)
-    return a.y_bf16 ? by_tiles<X, 1, false, SRC>(a, st) : by_tiles<X, 1, true, SRC>(a, st);
+    return by_tiles<X, 1, SRC>(a, st);
   else
-    return a.y_bf16 ? by_tiles<X, 2, false, SRC>(a, st) : by_tiles<X, 3, true, SRC>(a, st);
+    return a.y_bf16 ? by_tiles<X, 2, SRC>(a, st) : by_tiles<X, 3, SRC>(a, st);
 }
 
 template <typename X>

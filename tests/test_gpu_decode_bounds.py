@@ -1,0 +1,52 @@
+"""The few-row linears where a result is far smaller than its terms, against 64 bits: what is held on the way shows
+there, and not in results that are rounded to bf16 next to a large value.
+
+Every product of a piece of an activation (8 bits) and a code (4 bits) is exact in fp32.  A window of 128 codes is summed in
+fp32, then windows, waves and the bias: at most 128 * 3 pieces + K / 128 + 16 additions, each off by 2 u of the sum of
+absolute terms at the most (the matrix cores may cut instead of rounding), u = 2^-24."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_decode import BF, DT, U, dev, gen, hadamard64, qv, random_weights  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+def pack(q):
+    return (q[:, 0::2] & 15 | q[:, 1::2] << 4).view(torch.uint8).contiguous()
+
+
+def linear(qv, dev, X, q, ws, group, rotate, yt, epi=0):
+    M, K = X.shape
+    Y = torch.empty((M, q.shape[0]), dtype=DT[yt], device=dev)
+    if rotate:
+        work = torch.empty(max(1, qv.qv_w4a16_linear_workspace_size(M, K)), dtype=torch.uint8, device=dev)
+        qv.qv_w4a16_linear(X.to(dev), None, pack(q).to(dev), ws.to(dev), group, None, Y, work, epi)
+    else:
+        qv.qv_w4a16_gemv(X.to(dev), pack(q).to(dev), ws.to(dev), group, None, Y, epi)
+    return Y.double().cpu()
+
+
+@pytest.mark.parametrize("size", [1e5, 1e6, 1e7, 1e37])
+@pytest.mark.parametrize("M,K,N,group,xt", [
+    (1, 1024, 64, 128, "bf16"), (5, 2048, 700, 256, "bf16"), (16, 4096, 900, 4096, "bf16"), (3, 4096, 2500, 512, "bf16"),
+    (20, 1024, 4100, 128, "bf16"), (4, 1024, 9000, 128, "bf16"), (16, 1024, 17000, 1024, "bf16"), (2, 1024, 100, 128, "fp32"),
+])
+def test_outlier_against_zero_codes(qv, dev, M, K, N, group, xt, size):
+    """A large activation whose codes are zero adds exactly nothing to a bf16 result."""
+    g = gen(K + N)
+    q, _, ws = random_weights(N, K, group, g)
+    X = torch.randn((M, K), generator=g)
+    at = torch.randint(K, (3,), generator=g)
+    q[:, at] = 0
+    X[:, at] = size * torch.tensor([1.0, -1.0, 0.77])
+    X = X.to(DT[xt])
+    Y = linear(qv, dev, X, q, ws, group, False, "bf16")
+    w = q.double() * ws.double().repeat_interleave(group, 1)
+    y, terms = X.double() @ w.t(), X.double().abs() @ w.abs().t()
+    tol = BF * 1.01 * y.abs() + 2 * (3 * 128 + K / 128 + 16) * U * terms
+    worst = ((Y - y).abs() / tol).max().item()
+    assert worst <= 1.0, f"{worst:.2f} of the bound"
