@@ -18,8 +18,8 @@
 //     24 sum_k x[m][k] taken off each group's sum, would round every sum at the size of 24 |x|: a large activation against
 //     a code of zero has to add nothing.
 //   - an activation is a sum of NP bf16 pieces (the top 16 bits, then the top 16 bits of the rest, ...):
-//     one piece is exact for bf16 rows, two keep 16 bits for rotated or fp32 rows with a bf16 result
-//     (2^-16 against the result's own 2^-8), three keep all 24 bits for fp32 results.
+//     one piece is exact for bf16 rows, three are for fp32 and rotated rows (all 24 bits, whatever the result's type: two
+//     would leave up to 2^-15 of each, all of one sign).
 // A lane's 16-byte load holds 32 codes of one channel, and code i of dword j is contracted in MFMA j;
 // the order of k inside the sum is free, so activations are read to match: lane (row r, quarter c)
 // takes k = 32 c + 8 j + i of the 128-code window.
@@ -619,8 +619,8 @@ hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
   }
   // Two blocks of 32 channels share a CU where their registers (bf16 rows) and LDS (rotated rows) allow it; with more than
   // a few rows, reading the rows twice costs more than that gives: K = 4096, N = 16384, rows read and 1, 8, 16 of them 10.6, 11.4,
-  // 12.8 us (64 channels: 11.6, 12.0, 12.9), rotated and 1, 4 of them 13.0, 21.0 us (14.5, 16.3).
-  const bool two = sizeof(X) == 2 && a.M <= (SRC == kStaged ? 8 : 3);
+  // 12.8 us (64 channels: 11.6, 12.0, 12.9), rotated and 1, 2, 3 of them 13.4, 14.5, 20.6 us (64 channels, 3: 16.5).
+  const bool two = sizeof(X) == 2 && a.M <= (SRC == kStaged ? 8 : (SRC == kRot1024 ? 3 : 2));
   if (!fits(kRows, 32, two ? 2 : 1)) return launch_kernel<X, NP, 1, 4, 1, SRC>(a, st);
   if (!fits(kRows, 16)) return launch_kernel<X, NP, 1, 2, 1, SRC>(a, st);
   if constexpr (SRC != kRot1024) {  // K = 1024 has 8 windows, one for each wave
@@ -630,13 +630,10 @@ hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
   return launch_kernel<X, NP, 1, 1, 1, SRC>(a, st);
 }
 
-// Pieces by the types: rows that are bf16 are one piece; others two or, for fp32 results, three.
+// Pieces by the type: rows that are bf16 are one piece, others three.
 template <typename X, int SRC>
 hipError_t by_types(const Args<X>& a, hipStream_t st) {
-  if constexpr (sizeof(X) == 2 && kWidth<SRC> == 0)
-    return by_tiles<X, 1, SRC>(a, st);
-  else
-    return a.y_bf16 ? by_tiles<X, 2, SRC>(a, st) : by_tiles<X, 3, SRC>(a, st);
+  return by_tiles<X, sizeof(X) == 2 && kWidth<SRC> == 0 ? 1 : 3, SRC>(a, st);
 }
 
 template <typename X>

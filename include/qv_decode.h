@@ -35,8 +35,8 @@ extern "C" {
  *   w_scale  [N][K / group] fp32 (qv_pack_weights_grouped; with group = K: qv_pack_weights).
  *   bias     [N] fp32 or NULL.   epi  QV_EPI_NONE or QV_EPI_GELU (0.5 y erfc(-y / sqrt 2)).
  *   Y        [M][ldy] fp32 or bf16, rounded once, to nearest even; ldy >= N, any (rows need no alignment).
- * The products are exact to fp32: an fp32 activation is split into bf16 pieces that sum to it (two
- * pieces, 16 bits, where Y is bf16; three, all 24 bits, where Y is fp32), products and sums are fp32.
+ * Every product of an activation and a code is exact (an fp32 or rotated activation is split into three bf16
+ * pieces that sum to it), sums are fp32.
  */
 qv_status qv_w4a16_gemv(const void* X, qv_dtype x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* Wq,
                         const float* w_scale, int64_t group, const float* bias, int64_t N, qv_epilogue epi, void* Y,

@@ -50,3 +50,34 @@ def test_outlier_against_zero_codes(qv, dev, M, K, N, group, xt, size):
     tol = BF * 1.01 * y.abs() + 2 * (3 * 128 + K / 128 + 16) * U * terms
     worst = ((Y - y).abs() / tol).max().item()
     assert worst <= 1.0, f"{worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("xt,K,rotate", [("fp32", 128, False), ("fp32", 2048, False), ("fp32", 1024, True), ("fp32", 4096, True),
+                                         ("bf16", 1024, True), ("bf16", 4096, True)])
+@pytest.mark.parametrize("M", [1, 5, 17])
+def test_last_bits_of_an_activation(qv, dev, xt, K, rotate, M):
+    """Two activations that agree in their first bits cancel: a bf16 result shows the bits behind them, exactly.
+
+    Unrotated 1 + 2^-8 + 2^-17 and 1 + 2^-8; rotated, a row of three values a, b, c, whose elements are (+-a +- b +- c) /
+    sqrt K: those of the same signs for a and b and either sign for c differ by 2 c / sqrt K.  Every sum on the way is exact."""
+    N = 40
+    X = torch.zeros((M, K))
+    q = torch.zeros((N, K), dtype=torch.int8)
+    if rotate:
+        a, b, c = 1 + 2.0 ** -7, 2.0 ** -8 + 2.0 ** -15, 2.0 ** -17
+        at = (3, 5 + 8, K // 2 + 1)
+        X[:, at[0]], X[:, at[1]], X[:, at[2]] = a, b, c
+        h = hadamard64(K)[list(at)]
+        plus = ((h[0] > 0) & (h[1] > 0) & (h[2] > 0)).nonzero()[:, 0]
+        minus = ((h[0] > 0) & (h[1] > 0) & (h[2] < 0)).nonzero()[:, 0]
+        value = 2 * c / math.sqrt(K)
+    else:
+        plus, minus = torch.arange(0, 64, 2), torch.arange(1, 64, 2)
+        X[:, plus], X[:, minus] = 1 + 2.0 ** -8 + 2.0 ** -17, -(1 + 2.0 ** -8)
+        value = 2.0 ** -17
+    for n in range(N):
+        q[n, plus[n % len(plus)]] = 7
+        q[n, minus[(3 * n) % len(minus)]] = -7 if rotate else 7
+    ws = torch.full((N, K // 128), 0.5)
+    Y = linear(qv, dev, X.to(DT[xt]), q, ws, 128, rotate, "bf16")
+    assert bool((Y == 3.5 * value).all()), (Y / (3.5 * value)).unique()
