@@ -14,8 +14,8 @@
 //   S^T = K q^T     lane (r = lane % 16, c = lane / 16) loads 16 bytes of token r's key as they lie in memory; it gets
 //                   the scores of tokens 4 c + i (i < 4) for query r.
 //   O^T += V^T P^T  over 32 tokens, slots 8 c + 4 u + i being token 4 c + i of tile u: so a lane's own scores are its operand,
-//                   in bf16 pieces that sum to them (two pieces, 16 bits, for bf16 results, three for fp32; one piece's
-//                   2^-9 would show).  The other operand is value channel D / 16 r + e of the same tokens: each lane
+//                   in three bf16 pieces that sum to them (two would leave up to 2^-15 of each, always of its sign, while the
+//                   sum that divides the result takes it whole).  The other operand is value channel D / 16 r + e of the same tokens: each lane
 //                   loads D / 16 neighbouring channels of four tokens a tile and picks channel e of a pair of tokens with one
 //                   byte permutation.  The result has query r in lane (r, c), channels 4 D / 16 c onwards, next
 //                   to that query's maximum and sum.
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
   constexpr int kE = D / 16;
   constexpr int kElem = INT8 ? 1 : 2;
   constexpr int kU = 2;  // tiles at a time
-  constexpr int NV = sizeof(X) == 2 ? 2 : 3;  // bf16 pieces of a probability
+  constexpr int NV = 3;  // bf16 pieces of a probability
   constexpr int kRowsOut = ONE ? 1 : kTile;
   __shared__ float red_o[W][kRowsOut][D + 4];
   __shared__ float red_m[W][kRowsOut], red_l[W][kRowsOut];

@@ -1,0 +1,57 @@
+"""The attention where a result is far smaller than its terms, and where it is not a number."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_decode import DT, U, attend, dev, fill, gen, make_cache, qv, shuffled_table  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind,dim,share", [("bf16", 64, 2), ("bf16", 128, 4), ("int8", 64, 4), ("int8", 128, 2),
+                                            ("bf16", 64, 1), ("int8", 128, 1)])
+def test_probabilities_keep_their_bits(qv, dev, xt, kind, dim, share):
+    """One token of probability p = exp(t) and value -1 against tokens of probability 1 whose values sum to p.
+
+    A score of up to 4 bits is off by 2 roundings of u each, times ln 2; exp2 by 2 u; products and sums of five tokens by
+    a dozen more: 32 u of the sum of p |v|, and twice that for sums that the matrix cores cut."""
+    B = 24
+    t = -torch.linspace(0.1, 2.7, B).to(torch.bfloat16).double()  # a score: channel 0 of the token's key
+    table = torch.arange(B, dtype=torch.int32)[:, None]
+    cache = make_cache(qv, dev, B, 1, 16, dim, kind, 0)
+    p = torch.exp(t)
+    zero = torch.zeros(dim, device=dev)
+    value = torch.zeros((B, 5), dtype=torch.float64)
+    for b in range(B):
+        rest = p[b].item()
+        for i in range(5):
+            code = -1.0 if i == 0 else 0.0
+            scale = 1.0
+            if 0 < i < 4:  # a third of p at a time, in as many bits as the cache has
+                part = rest / (4 - i)
+                if kind == "bf16":
+                    code = torch.tensor(rest).to(torch.bfloat16).item()
+                else:
+                    code, scale = 3.0, torch.tensor(part / 3).float().item()
+                rest -= code * scale
+            value[b, i] = code * scale
+            key = zero.clone()
+            if kind == "bf16":
+                key[0] = t[b] if i == 0 else 0.0
+            else:
+                key[0] = -1 if i == 0 else 0
+                cache.k_scale[b, 0, i] = -t[b] if i == 0 else 1.0
+                cache.v_scale[b, 0, i] = scale
+            cache.k_pages[b, 0, i] = key.to(cache.k_pages.dtype)
+            cache.v_pages[b, 0, i] = (zero + code).to(cache.v_pages.dtype)
+    Q = torch.zeros((B, share, dim))
+    Q[:, :, 0] = 1.0
+    O = attend(qv, dev, Q.to(DT[xt]).to(dev), cache, table.to(dev), [5] * B, scale=1.0).double().cpu()
+    weight = torch.cat((p[:, None], torch.ones((B, 4), dtype=torch.float64)), 1)
+    o = ((weight * value).sum(1) / weight.sum(1))[:, None, None]
+    terms = ((weight * value.abs()).sum(1) / weight.sum(1))[:, None, None]
+    worst = ((O - o).abs() / (64 * U * terms + 2.0 ** -8 * o.abs())).max().item()
+    assert worst <= 1.0, f"{worst:.2f} of the bound"
