@@ -26,6 +26,9 @@
 // second product is D / 16 fp32 multiply-adds a token.
 // The next unit's keys are loaded as soon as this one's scores are formed, its values as soon as this one's sum is.
 //
+// A row without tokens is one whose sum is zero: fmaxf passes over a score that is NaN, exp2 makes it a probability of NaN, and
+// sum and result are NaN as well.
+//
 // The tokens of all sequences together are cut into parts of equal size, one round of the blocks that the chip holds at once,
 // or more where each part still has kLongPart tokens; a second kernel joins a sequence's parts by their maxima and
 // sums.  Measured with one, two and three rounds: ragged batch 60, 58, 61 us, long int8 48, 55, 59, 4 sequences up to
@@ -385,7 +388,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
   for (int unit = 0; unit < units; ++unit) {
     const int tile0 = mine_first + unit * (W * kU), tile1 = tile0 + W * kU;
     const bool more = unit + 1 < units;
-    float s[kU][4];
+    float s[kU][4];  // -inf: the token takes no part
     float top = m;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -445,7 +448,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
       for (int i = 0; i < 4; ++i) {
         float p = exp2_raw(s[u][i] - m);
         l += p;
-        if constexpr (INT8) p = p > 0.0f ? p * vs[u][i] : 0.0f;  // behind a sequence's end a scale may be anything
+        if constexpr (INT8) p = s[u][i] != -INFINITY ? p * vs[u][i] : 0.0f;  // behind a sequence's end a scale may be anything
         s[u][i] = p;
       }
       if (here[u] < 0) {
@@ -527,7 +530,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
     }
     const uint32_t head = h * a.share + q0 + j;
     if (part.count == 1) {
-      store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, sum > 0.0f ? val / sum : 0.0f);
+      store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, sum == 0.0f ? 0.0f : val / sum);
     } else {
       const int64_t to = (int64_t)number * a.q_heads + head;
       a.partial[to * D + d] = val;
@@ -596,7 +599,7 @@ __global__ __launch_bounds__(64 * W) void join_kernel(Args a) {
     float x = sums[0][d];
 #pragma unroll
     for (int w = 1; w < W; ++w) x += sums[w][d];
-    store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, l > 0.0f ? x / l : 0.0f);
+    store(static_cast<X*>(a.o) + b * a.o_ts + (int64_t)head * a.o_hs + d, l == 0.0f ? 0.0f : x / l);
   }
 }
 

@@ -135,7 +135,8 @@ size_t qv_paged_attention_workspace_size(int64_t B, int64_t q_heads, int64_t hea
  *   page_table  as for qv_kv_append, B rows.  Tokens on a page outside [0, num_pages) do not take part
  *               (a page may be given back once a window has left it behind).
  *   lens        [B] int32 tokens of each sequence, the new one included; cut to [0, max_pages * page_size].
- *               A sequence with no token gives zeros.  What the cache holds behind them is not used.
+ *               A sequence with no token gives zeros.  What the cache holds behind them is not used.  A query of NaN
+ *               (qv_kv_append makes them), or a NaN among the tokens, gives NaN.
  *   O           [B][q_heads][head_dim] of Q's type.  Scores, softmax and sums are fp32; probabilities are
  *               not rounded, and an fp32 query is taken as three bf16 pieces that sum to it.
  *   workspace   at least qv_paged_attention_workspace_size(B, q_heads, heads, head_dim, max_pages *

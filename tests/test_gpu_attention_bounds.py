@@ -55,3 +55,38 @@ def test_probabilities_keep_their_bits(qv, dev, xt, kind, dim, share):
     terms = ((weight * value.abs()).sum(1) / weight.sum(1))[:, None, None]
     worst = ((O - o).abs() / (64 * U * terms + 2.0 ** -8 * o.abs())).max().item()
     assert worst <= 1.0, f"{worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("xt,kind,dim,share", [("bf16", "bf16", 64, 1), ("fp32", "bf16", 128, 3), ("bf16", "int8", 128, 8),
+                                               ("fp32", "int8", 64, 1), ("bf16", "bf16", 128, 17)])
+@pytest.mark.parametrize("longest", [40, 3000])
+def test_what_is_not_a_number_stays_so(qv, dev, xt, kind, dim, share, longest):
+    """A query, a key or a value of NaN gives NaN, in its own rows only; what no row attends to has no effect, and a sequence
+    without tokens still gives zeros."""
+    g = gen(longest + dim)
+    lens = [longest, 0, longest - 3, 20, longest, 31]
+    table, pages = shuffled_table(lens, 16, g)
+    cache = make_cache(qv, dev, pages, 2, 16, dim, kind, 0)  # NaN behind every sequence's end
+    fill(cache, table, lens, g)
+    Q = torch.randn((6, 2 * share, dim), generator=g).to(DT[xt]).to(dev)
+    clean = attend(qv, dev, Q, cache, table.to(dev), lens).clone()
+    assert bool(torch.isfinite(clean.float()).all()) and bool((clean[1] == 0).all())
+
+    def spoil(pages_, scales, b, t, head, channel):
+        page, slot = int(table[b, t // 16]), t % 16
+        if scales is None:
+            pages_[page, head, slot, channel] = float("nan")
+        else:
+            scales[page, head, slot] = float("nan")
+
+    Q[0, share] = float("nan")  # one query of the second head
+    Q[1, 0, 3] = float("nan")   # of a sequence without tokens
+    spoil(cache.k_pages, cache.k_scale, 2, longest - 10, 0, 5)
+    spoil(cache.v_pages, cache.v_scale, 3, 7, 1, 9)
+    O = attend(qv, dev, Q, cache, table.to(dev), lens).float().cpu()
+    bad = torch.zeros(O.shape, dtype=torch.bool)
+    bad[0, share] = True
+    bad[2, :share] = True
+    bad[3, share:, slice(9, 10) if kind == "bf16" else slice(None)] = True
+    assert bool(torch.isnan(O[bad]).all())
+    assert torch.equal(O[~bad], clean.float().cpu()[~bad])
