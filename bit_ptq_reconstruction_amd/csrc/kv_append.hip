@@ -47,6 +47,7 @@ struct Args {
 };
 
 __device__ __forceinline__ float bits_float(unsigned u) { return __builtin_bit_cast(float, u); }
+__device__ __forceinline__ unsigned float_bits(float f) { return __builtin_bit_cast(unsigned, f); }
 
 __device__ __forceinline__ void load8(const __hip_bfloat16* p, float (&v)[8]) {
   const u32x4 d = *reinterpret_cast<const u32x4*>(p);
@@ -76,7 +77,7 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
   reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
 }
-// Codes of the correctly rounded quotients v / scale (scale 0: zeros).  The product with the reciprocal is off by at most
+// Codes of the correctly rounded quotients v / scale (scale 0 or NaN: zeros).  The product with the reciprocal is off by at most
 // 127 * 2^-23 and the quotient by 127 * 2^-24, 2.3e-5 together: only values nearer than 3e-5 to a half need the
 // division itself (0.4 % of the waves' elements).
 __device__ __forceinline__ void store8(int8_t* p, const float (&v)[8], float scale, float inverse) {
@@ -86,7 +87,7 @@ __device__ __forceinline__ void store8(int8_t* p, const float (&v)[8], float sca
     const float t = v[i] * inverse;
     float q = rintf(t);
     if (fabsf(t - q) > 0.49997f) q = rintf(v[i] / scale);
-    q = fminf(fmaxf(q, -128.0f), 127.0f);
+    q = inverse > 0.0f ? fminf(fmaxf(q, -128.0f), 127.0f) : 0.0f;
     w[i >> 2] |= ((unsigned)(int)q & 255u) << (8 * (i & 3));
   }
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
@@ -174,13 +175,15 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Args a) {
     }
     float scale = 0.0f;
     if constexpr (INT8) {
-      float top = 0.0f;
+      // The maximum as bits, which for magnitudes have the order of the values, infinities and then NaN above all.
+      unsigned bits = 0;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) top = fmaxf(top, fmaxf(fabsf(lo[i][n]), fabsf(hi[i][n])));
+      for (int n = 0; n < 8; ++n) bits = max(bits, max(float_bits(lo[i][n]) & 0x7FFFFFFFu, float_bits(hi[i][n]) & 0x7FFFFFFFu));
 #pragma unroll
-      for (int d = 1; d < kParts; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-      scale = top / 127.0f;
-      if (!(scale >= 1.17549435e-38f)) scale = 0.0f;  // zero and subnormal scales
+      for (int d = 1; d < kParts; d <<= 1) bits = max(bits, (unsigned)__shfl_xor((int)bits, d));
+      scale = bits_float(bits) / 127.0f;
+      if (scale < 1.17549435e-38f) scale = 0.0f;  // zero and subnormal scales
+      if (bits >= 0x7F800000u) scale = __builtin_nanf("");
     }
     if (!stored || kind[i] == 0 || kind[i] == 3) continue;
     const int64_t to = page * a.page_stride + head[i] * a.head_stride + slot * a.token_stride;
@@ -191,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(Args a) {
       store8(o + hi_c, hi[i]);
     } else {
       int8_t* o = reinterpret_cast<int8_t*>(base) + to;
-      const float inverse = scale > 0.0f ? 1.0f / scale : 0.0f;  // 0: every code is 0
+      const float inverse = scale > 0.0f ? 1.0f / scale : 0.0f;  // 0: every code is 0, of NaN and infinities too
       store8(o + lo_c, lo[i], scale, inverse);
       store8(o + hi_c, hi[i], scale, inverse);
       if (part == 0) (kind[i] == 1 ? a.ks : a.vs)[(page * a.heads + head[i]) * a.page_size + slot] = scale;

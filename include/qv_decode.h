@@ -113,7 +113,8 @@ typedef struct {
  *               Q_out may be Q itself with the same strides.
  * bf16 caches round the rotated value once, to nearest even.  int8 caches take the scale of each
  * (token, head) from its rotated fp32 values: scale = max |x| / 127, code = clamp(rne(x / scale), -128,
- * 127), both quotients correctly rounded; a zero or subnormal scale becomes 0 with zero codes.
+ * 127), both quotients correctly rounded; a zero or subnormal scale becomes 0 with zero codes, and a row that
+ * is not finite gets a scale of NaN with zero codes.
  */
 qv_status qv_kv_append(const qv_kv_cache* cache, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
                        int64_t ld_table, const int32_t* token_seq, const int32_t* token_index, int64_t T,

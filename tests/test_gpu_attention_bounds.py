@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_decode import DT, U, attend, dev, fill, gen, make_cache, qv, shuffled_table  # noqa: E402,F401
+from test_gpu_decode import DT, U, attend, codes32, dev, fill, gen, make_cache, qv, shuffled_table  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,30 @@ def test_what_is_not_a_number_stays_so(qv, dev, xt, kind, dim, share, longest):
     bad[3, share:, slice(9, 10) if kind == "bf16" else slice(None)] = True
     assert bool(torch.isnan(O[bad]).all())
     assert torch.equal(O[~bad], clean.float().cpu()[~bad])
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_int8_append_of_what_is_not_finite(qv, dev, xt, dim):
+    """A token and head with a NaN or an infinity is stored with a scale of NaN and zero codes, its neighbours as they are; the
+    attention that reads it gives NaN."""
+    g = gen(dim)
+    cache = make_cache(qv, dev, 2, 3, 16, dim, "int8", 0)
+    K, V = (torch.randn((20, 3, dim), generator=g) for _ in range(2))
+    V[3, 1, dim - 1], V[7, 0, 0], V[7, 2, 17], K[11, 2, 8] = float("nan"), float("inf"), float("-inf"), float("nan")
+    K, V = K.to(DT[xt]), V.to(DT[xt])
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device=dev)
+    i = torch.arange(20, dtype=torch.int32, device=dev)
+    qv.qv_kv_append(cache, table, torch.zeros_like(i), i, K.to(dev), V.to(dev))
+    for pages, scales, x, bad in ((cache.k_pages, cache.k_scale, K, [(11, 2)]),
+                                  (cache.v_pages, cache.v_scale, V, [(3, 1), (7, 0), (7, 2)])):
+        codes, scale = codes32(x.float())
+        for t, h in bad:
+            codes[t, h], scale[t, h] = 0, float("nan")
+        order = lambda p: torch.cat((p[1], p[0]), 1)[:, :20].transpose(0, 1).cpu()
+        assert torch.equal(order(pages), codes)
+        assert torch.equal(torch.isnan(order(scales)), torch.isnan(scale))
+        assert torch.equal(torch.nan_to_num(order(scales)), torch.nan_to_num(scale))
+    Q = torch.randn((1, 3, dim), generator=g).to(DT[xt]).to(dev)
+    n = lambda *lens: torch.isnan(attend(qv, dev, Q, cache, table, list(lens)).float()).all(2).tolist()
+    assert n(3) == [[False, False, False]] and n(4) == [[False, True, False]] and n(20) == [[True, True, True]]
