@@ -275,6 +275,7 @@ PyObject* kv_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (v.scalar_type() != k.scalar_type() || !v.sizes().equals(k.sizes()) || !v.strides().equals(k.strides()))
       c.bad("v_pages", v, "type, shape and strides of k_pages");
     const int64_t D = k.size(3);
+    if (k.size(1) == 0 || k.size(2) == 0 || D == 0) c.bad("k_pages", k, "at least one head, token and channel");
     if (k.stride(3) != 1 && D > 1) c.bad("k_pages", k, "unit channel stride");
     int64_t stride[3];
     for (int i = 0; i < 3; ++i) {
@@ -386,6 +387,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &Q = c.tensor("Q", a[0]), &table = c.tensor("page_table", a[2]), &lens = c.tensor("lens", a[3]),
                      &O = c.tensor("O", a[4]), &work = c.tensor("workspace", a[5]);
     const int64_t D = kv.c.head_dim;
+    if (kv.c.heads <= 0) c.bad("the cache has no heads");
     if (Q.dim() != 3 || Q.size(1) == 0 || Q.size(1) % kv.c.heads != 0 || Q.size(2) != D)
       c.bad("Q", Q, "[B, a multiple of " + std::to_string(kv.c.heads) + " heads, " + std::to_string(D) + "]");
     const int64_t B = Q.size(0), Hq = Q.size(1);
