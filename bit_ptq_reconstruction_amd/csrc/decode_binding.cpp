@@ -17,6 +17,7 @@
 #include <string>
 
 #include "qv_decode.h"
+#include "qv_decode_internal.h"
 
 namespace {
 
@@ -97,6 +98,13 @@ struct Call {
       bad(name, t, "shape " + shape_text({T, H, D}));
     if (t.stride(2) != 1 || (t.stride(1) < D && H > 1)) bad(name, t, "unit channel stride and heads that do not overlap");
     return {t.data_ptr(), T > 1 ? t.stride(0) : 0, H > 1 ? t.stride(1) : D};
+  }
+
+  // The same for rows that are written.
+  qv_heads output(const char* name, const at::Tensor& t, int64_t T, int64_t H, int64_t D, qv_dtype type) const {
+    const qv_heads h = heads(name, t, T, H, D, type);
+    if (qv::rows_overlap(T, h.token_stride, H, h.head_stride, D)) bad(name, t, "tokens and heads that do not overlap");
+    return h;
   }
 
   // Row stride of a page table [rows, pages].
@@ -366,7 +374,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Hq = Q->dim() == 3 ? Q->size(1) : 0;
       if (Hq == 0) c.bad("Q", *Q, "[T, q_heads, D]");
       q = c.heads("Q", *Q, T, Hq, D, type);
-      qo = c.heads("Q_out", *Qo, T, Hq, D, type);
+      qo = c.output("Q_out", *Qo, T, Hq, D, type);
     }
     for (const at::Tensor* t : {&table, &index, &K, &V, opt[0], opt[1], opt[2], opt[3], Q, Qo})
       if (t) c.on_gpu(*t);
@@ -392,7 +400,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       c.bad("Q", Q, "[B, a multiple of " + std::to_string(kv.c.heads) + " heads, " + std::to_string(D) + "]");
     const int64_t B = Q.size(0), Hq = Q.size(1);
     const qv_dtype type = c.float_type("Q", Q);
-    const qv_heads q = c.heads("Q", Q, B, Hq, D, type), o = c.heads("O", O, B, Hq, D, type);
+    const qv_heads q = c.heads("Q", Q, B, Hq, D, type), o = c.output("O", O, B, Hq, D, type);
     const int64_t ld = c.table(table);
     if (table.size(0) != B) c.bad("page_table", table, std::to_string(B) + " rows");
     c.dense("lens", lens, at::kInt, {B});

@@ -72,6 +72,11 @@ qv_status check_heads(const qv_heads* h, qv_dtype t, int64_t D) {
   return QV_OK;
 }
 
+// Rows that are written: no two of them share memory.
+qv_status check_output(const qv_heads* h, int64_t T, int64_t H, int64_t D) {
+  return qv::rows_overlap(T, h->token_stride, H, h->head_stride, D) ? QV_ERR_SHAPE : QV_OK;
+}
+
 qv_status check_table(const int32_t* table, int64_t rows, int64_t max_pages, int64_t ld, const qv_kv_cache* c) {
   if (rows < 0 || max_pages < 0 || ld < max_pages || ld > kMaxDim) return QV_ERR_SHAPE;
   // places are counted in 32 bits
@@ -154,6 +159,8 @@ qv_status qv_kv_append(const qv_kv_cache* cache, const int32_t* page_table, int6
       st = check_heads(h, x_dtype, cache->head_dim);
       if (st != QV_OK) return st;
     }
+    if (Q_out) st = check_output(Q_out, T, q_heads, cache->head_dim);
+    if (st != QV_OK) return st;
     qv::AppendArgs a = {};
     a.cache = *cache;
     a.page_table = page_table;
@@ -212,6 +219,8 @@ qv_status qv_paged_attention(const qv_heads* Q, qv_dtype q_dtype, int64_t B, int
       st = check_heads(h, q_dtype, cache->head_dim);
       if (st != QV_OK) return st;
     }
+    st = check_output(O, B, q_heads, cache->head_dim);
+    if (st != QV_OK) return st;
     const size_t need =
         qv_paged_attention_workspace_size(B, q_heads, cache->heads, cache->head_dim, max_pages * cache->page_size);
     if (!workspace || need == 0 || workspace_bytes < need) return QV_ERR_WORKSPACE;

@@ -15,6 +15,19 @@ hipError_t launch_w4a16(const void* X, bool x_bf16, int64_t M, int64_t K, int64_
                         const uint8_t* Wq, const float* ws, int64_t group, const float* bias, int64_t N, bool gelu,
                         void* Y, bool y_bf16, int64_t ldy, float* rows32, hipStream_t st);
 
+// Whether two of the rows of D elements at t token_stride + h head_stride (t < T, h < H) share an element.
+inline bool rows_overlap(int64_t T, int64_t token_stride, int64_t H, int64_t head_stride, int64_t D) {
+  if (H > 1 && head_stride < D) return T > 0;
+  if (T <= 1 || H < 1) return false;
+  if (token_stride < D) return true;
+  if (token_stride >= (H - 1) * head_stride + D || token_stride <= (head_stride - D) / (T - 1)) return false;  // nested
+  for (int64_t h = 1; h < H; ++h) {  // the tokens on either side of head h of token 0
+    const int64_t at = h * head_stride, before = at / token_stride, gap = at - before * token_stride;
+    if ((before >= 1 && before < T && gap < D) || (before + 1 < T && token_stride - gap < D)) return true;
+  }
+  return false;
+}
+
 struct AppendArgs {
   qv_kv_cache cache;
   const int32_t* page_table;

@@ -85,7 +85,8 @@ typedef struct {
 } qv_kv_cache;
 
 /* Input rows [T][heads][head_dim] with unit channel stride: token t, head h at t token_stride +
- * h head_stride (a slice of a packed qkv tensor fits).  16-byte aligned, strides multiples of 16 bytes. */
+ * h head_stride (a slice of a packed qkv tensor fits).  16-byte aligned, strides multiples of 16 bytes; rows that are
+ * written must not overlap (QV_ERR_SHAPE). */
 typedef struct {
   const void* data;
   int64_t token_stride;

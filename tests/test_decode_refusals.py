@@ -7,7 +7,9 @@ torch = pytest.importorskip("torch")
 
 import bit_ptq_reconstruction_amd as qv  # noqa: E402
 from bit_ptq_reconstruction_amd.decode import QVKVCacheStruct  # noqa: E402
-from test_decode_binding import append, attend, bf, built, refused  # noqa: E402,F401
+from test_decode_abi import SHAPE, WORKSPACE, L  # noqa: E402,F401
+from test_decode_abi import append as abi_append, attend as abi_attend, heads as abi_heads  # noqa: E402
+from test_decode_binding import append, attend, bf, built, i32, refused  # noqa: E402,F401
 
 
 def handle(heads=2, device=-1):
@@ -31,3 +33,41 @@ def test_cache_without_heads(shape):
     refused(attend, "no heads", cache=none)
     refused(attend, "no heads", cache=none, Q=bf(3, 0, 64), O=bf(3, 0, 64))
     refused(append, "GPU tensor", cache=none, K=bf(5, 0, 64), V=bf(5, 0, 64))
+
+
+def overlap(T, ts, H, hs, D):
+    """Rows of D elements at t ts + h hs, counted out."""
+    seen = set()
+    for t in range(T):
+        for h in range(H):
+            row = set(range(t * ts + h * hs, t * ts + h * hs + D))
+            if row & seen:
+                return True
+            seen |= row
+    return False
+
+
+def test_overlapping_outputs():
+    """Outputs expanded along the tokens, or laid out so that rows share memory, are refused; inputs may be."""
+    same = torch.zeros((1, 6, 64), dtype=torch.bfloat16)
+    refused(attend, "O is bfloat16 .* do not overlap", O=same.expand(3, 6, 64))
+    refused(append, "Q_out is bfloat16 .* do not overlap", Q_out=same.expand(5, 6, 64))
+    refused(attend, "GPU tensor", Q=same.expand(3, 6, 64))
+    refused(append, "GPU tensor", Q=same.expand(5, 6, 64))
+    flat = bf(1 << 14)
+    refused(attend, "O is bfloat16 .* do not overlap", O=flat.as_strided((3, 6, 64), (64, 64, 1)))
+    refused(attend, "O is bfloat16 .* do not overlap", O=flat.as_strided((3, 6, 64), (192, 128, 1)))
+    refused(attend, "GPU tensor", O=flat.as_strided((3, 6, 64), (64, 192, 1)))     # heads outside tokens
+    refused(attend, "GPU tensor", O=flat.as_strided((2, 2, 64), (192, 128, 1)), Q=bf(2, 2, 64), page_table=i32(2, 4),
+            lens=i32(2))                                                          # 0, 128, 192, 320
+
+
+def test_overlapping_outputs_of_the_library(L):
+    """Every small layout, against the rows counted out."""
+    for T, H in ((1, 2), (2, 2), (2, 4), (3, 2), (5, 4)):
+        for ts in range(0, 449, 64):
+            for hs in range(64, 449, 64):
+                bad = overlap(T, ts, H, hs, 64)
+                got = abi_attend(L, O=abi_heads(ts=ts, hs=hs), Q=abi_heads(ts=256), B=T, q_heads=H, size=0)
+                assert got == (SHAPE if bad else WORKSPACE), (T, H, ts, hs)
+    assert abi_append(L, Q_out=abi_heads(ts=0)) == SHAPE and abi_append(L, Q_out=abi_heads(ts=64, hs=256)) == SHAPE
