@@ -159,6 +159,12 @@ qv_epilogue epilogue(PyObject* o) {
 
 void* address(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
+// Of a table, whose address says that there is one: a tensor without elements has none of its own.
+const float* table_address(const at::Tensor* t) {
+  alignas(16) static const float none[4] = {};
+  return t && t->numel() == 0 ? none : (const float*)address(t);
+}
+
 PyObject* qv_error = nullptr;  // the package's QVError
 
 PyObject* done(const Call& c, qv_status st) {
@@ -381,7 +387,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::hip::HIPGuard on((c10::DeviceIndex)c.device);
     return done(c, qv_kv_append(&kv.c, (const int32_t*)table.data_ptr(), table.size(0), table.size(1), ld,
                                 (const int32_t*)address(opt[0]), (const int32_t*)index.data_ptr(), T, &k, &v, type,
-                                (const float*)address(opt[1]), (const float*)address(opt[2]), places, axes,
+                                table_address(opt[1]), table_address(opt[2]), places, axes,
                                 (const int32_t*)address(opt[3]), Q ? &q : nullptr, Q ? &qo : nullptr, Hq,
                                 c.stream(a[11])));
   });
