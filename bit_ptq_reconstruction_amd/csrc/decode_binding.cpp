@@ -82,7 +82,7 @@ struct Call {
     if (t.dim() != 2 || t.size(0) != M || t.size(1) != N) bad(name, t, "shape " + shape_text({M, N}));
     if ((t.stride(1) != 1 && N > 1) || (t.stride(0) < N && M > 1))
       bad(name, t, "unit column stride and a row stride of at least " + std::to_string(N));
-    return M > 1 ? t.stride(0) : (t.stride(0) < N ? N : t.stride(0));
+    return M > 1 ? t.stride(0) : N;  // a single row has no stride of its own
   }
 
   qv_dtype float_type(const char* name, const at::Tensor& t) const {

@@ -81,3 +81,17 @@ def test_last_bits_of_an_activation(qv, dev, xt, K, rotate, M):
     ws = torch.full((N, K // 128), 0.5)
     Y = linear(qv, dev, X.to(DT[xt]), q, ws, 128, rotate, "bf16")
     assert bool((Y == 3.5 * value).all()), (Y / (3.5 * value)).unique()
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp32"])
+def test_single_row_of_any_stride(qv, dev, xt):
+    """One row of a tensor whose row stride is odd: the stride of a single row counts for nothing."""
+    g = gen(7)
+    q, packed, ws = random_weights(24, 256, 128, g)
+    wide = torch.randn((3, 259), generator=g).to(DT[xt]).to(dev)
+    Y = torch.empty((3, 31), device=dev)
+    qv.qv_w4a16_gemv(wide[:1, :256], packed.to(dev), ws.to(dev), 128, None, Y[:1, :24])
+    y = wide[:1, :256].double().cpu() @ (q.double() * ws.double().repeat_interleave(128, 1)).t()
+    assert bool(((Y[:1, :24].double().cpu() - y).abs() <= 1e-4).all())
+    with pytest.raises(qv.QVError, match="ALIGN"):  # the next row is not aligned
+        qv.qv_w4a16_gemv(wide[:2, :256], packed.to(dev), ws.to(dev), 128, None, Y[:2, :24])
