@@ -13,6 +13,8 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t{1} << 40;   // as in qv_abi.cpp: byte counts stay inside int64
 constexpr int64_t kMaxInt = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;  // of a launch, along one dimension
+constexpr int64_t kMaxChannels = kMaxThreads / 512 * 64;  // blocks of 512 threads and 64 channels
 
 bool aligned(const void* p, uintptr_t to = 16) { return (reinterpret_cast<uintptr_t>(p) % to) == 0; }
 
@@ -32,7 +34,7 @@ qv_status check_w4a16(const void* X, qv_dtype xt, int64_t M, int64_t K, int64_t 
   if ((K % 128) != 0 || K > 65536) return QV_ERR_UNSUPPORTED;
   if (group != K && ((group != 128 && group != 256 && group != 512) || (K % group) != 0)) return QV_ERR_UNSUPPORTED;
   if (ldx < K || ldy < N || ldx > kMaxDim || ldy > kMaxDim) return QV_ERR_SHAPE;
-  if (M > kMaxInt || N > kMaxInt - 256) return QV_ERR_UNSUPPORTED;
+  if (M > kMaxInt || N > kMaxChannels) return QV_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return QV_OK;
   if (!X || !Wq || !ws || !Y) return QV_ERR_NULL;
   if (!aligned(X) || !aligned(Wq) || !aligned(ws) || !aligned(bias) || !aligned(Y) ||
@@ -75,6 +77,11 @@ qv_status check_heads(const qv_heads* h, qv_dtype t, int64_t D) {
 // Rows that are written: no two of them share memory.
 qv_status check_output(const qv_heads* h, int64_t T, int64_t H, int64_t D) {
   return qv::rows_overlap(T, h->token_stride, H, h->head_stride, D) ? QV_ERR_SHAPE : QV_OK;
+}
+
+// Whether the attention's launches hold the batch: 256 threads to a part of a sequence, at least 128 to a query head's join.
+bool attention_fits(int64_t B, int64_t q_heads, const qv::AttentionParts& p) {
+  return p.most * p.blocks <= kMaxThreads / 256 && (!p.split || B * q_heads <= kMaxThreads / 128);
 }
 
 qv_status check_table(const int32_t* table, int64_t rows, int64_t max_pages, int64_t ld, const qv_kv_cache* c) {
@@ -195,6 +202,7 @@ size_t qv_paged_attention_workspace_size(int64_t B, int64_t q_heads, int64_t hea
       (head_dim != 64 && head_dim != 128) || capacity < 0 || capacity > kMaxInt || B > kMaxInt / q_heads)
     return 0;
   const qv::AttentionParts p = qv::paged_attention_parts(B, q_heads, heads, capacity);
+  if (!attention_fits(B, q_heads, p)) return 0;
   if (!p.split) return 256;
   return round256(static_cast<size_t>(p.most * q_heads) * static_cast<size_t>(head_dim + 2) * 4 + 1);
 }
@@ -211,6 +219,8 @@ qv_status qv_paged_attention(const qv_heads* Q, qv_dtype q_dtype, int64_t B, int
     if (st != QV_OK) return st;
     if (q_heads <= 0 || q_heads > 65536 || q_heads % cache->heads != 0 || window < 0) return QV_ERR_SHAPE;
     if (B > kMaxInt / q_heads) return QV_ERR_UNSUPPORTED;
+    if (!attention_fits(B, q_heads, qv::paged_attention_parts(B, q_heads, cache->heads, max_pages * cache->page_size)))
+      return QV_ERR_UNSUPPORTED;
     if (B == 0) return QV_OK;
     if (!Q || !O || !lens) return QV_ERR_NULL;
     if (!aligned(lens, 4)) return QV_ERR_ALIGN;

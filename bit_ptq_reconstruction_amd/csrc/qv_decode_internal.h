@@ -67,12 +67,13 @@ constexpr int64_t kLongPart = 1536;         // tokens from which a block's start
 constexpr int64_t kManyBlocks = 4096;       // no less than a round of them
 struct AttentionParts {
   int64_t many, most;
+  int64_t blocks;  // of a part
   bool split;  // whether a sequence can have more than one
 };
 inline AttentionParts paged_attention_parts(int64_t B, int64_t q_heads, int64_t heads, int64_t capacity) {
-  const int64_t each = heads * ((q_heads / heads + kQueriesPerBlock - 1) / kQueriesPerBlock);  // blocks of a part
   AttentionParts p;
-  p.many = (kManyBlocks + each - 1) / each;
+  p.blocks = heads * ((q_heads / heads + kQueriesPerBlock - 1) / kQueriesPerBlock);
+  p.many = (kManyBlocks + p.blocks - 1) / p.blocks;
   p.split = capacity > kMinTokensPerPart;
   const int64_t full = (capacity + kMinTokensPerPart - 1) / kMinTokensPerPart;
   p.most = !p.split ? B : (B * full < p.many + B ? B * full : p.many + B);

@@ -641,12 +641,16 @@ hipError_t launch(const Args<X>& a, bool rotate, float* rows32, hipStream_t st) 
   if (!rotate) return by_types<X, kStaged>(a, st);
   if (a.K == 1024 && a.M <= kFused1024) return by_types<X, kRot1024>(a, st);
   if (a.K == 4096 && a.M <= kFused4096) return by_types<X, kRot4096>(a, st);
-  if (a.K == 1024)
-    rotate_rows_kernel<1024, X><<<(unsigned)a.M, 128, 0, st>>>(a.x, a.ldx, a.mult, rows32);
-  else
-    rotate_rows_kernel<4096, X><<<(unsigned)a.M, 512, 0, st>>>(a.x, a.ldx, a.mult, rows32);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  constexpr int64_t kStep = int64_t{1} << 20;  // rows of a launch, which holds fewer than 2^32 threads
+  for (int64_t m = 0; m < a.M; m += kStep) {
+    const unsigned rows = (unsigned)(a.M - m < kStep ? a.M - m : kStep);
+    if (a.K == 1024)
+      rotate_rows_kernel<1024, X><<<rows, 128, 0, st>>>(a.x + m * a.ldx, a.ldx, a.mult, rows32 + m * a.K);
+    else
+      rotate_rows_kernel<4096, X><<<rows, 512, 0, st>>>(a.x + m * a.ldx, a.ldx, a.mult, rows32 + m * a.K);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const Args<float> b = {rows32, nullptr, a.wq, a.ws, a.bias, a.y, a.M, a.K, a.ldy, a.N, a.K, a.group,
                          a.group_shift, a.gelu, a.y_bf16};
   return by_types<float, kStaged>(b, st);

@@ -30,7 +30,7 @@ extern "C" {
  * X is taken as it is (already rotated, or against weights that were never rotated).
  *   X        [M][ldx] fp32 or bf16; every M is accepted, and the kernel is made for M up to 16 or so.
  *   K        multiple of 128 in [128, 65536] (else QV_ERR_UNSUPPORTED).
- *   Wq       [N][K/2] packed int4 codes in the layout of qv.h;  N >= 1, any.
+ *   Wq       [N][K/2] packed int4 codes in the layout of qv.h;  N >= 1, any up to 2^29 - 64.
  *   group    128, 256 or 512 dividing K, or K itself (one scale per output channel).
  *   w_scale  [N][K / group] fp32 (qv_pack_weights_grouped; with group = K: qv_pack_weights).
  *   bias     [N] fp32 or NULL.   epi  QV_EPI_NONE or QV_EPI_GELU (0.5 y erfc(-y / sqrt 2)).
@@ -133,7 +133,9 @@ size_t qv_paged_attention_workspace_size(int64_t B, int64_t q_heads, int64_t hea
  * qv_paged_attention -- attention of one new token of each of B sequences over the paged cache:
  *   O[b][i] = sum_t softmax_t(scale Q[b][i] . k[t][i / (q_heads / heads)]) v[t][i / (q_heads / heads)]
  * over the tokens max(0, lens[b] - window) <= t < lens[b] (window = 0: all of them).
- *   Q           [B][q_heads][head_dim] fp32 or bf16;  q_heads a multiple of the cache's heads.
+ *   Q           [B][q_heads][head_dim] fp32 or bf16;  q_heads a multiple of the cache's heads.  B times the blocks
+ *               of a sequence (one for up to 16 query heads of a cache head) is below 2^24, B q_heads below 2^25 (else
+ *               QV_ERR_UNSUPPORTED).
  *   page_table  as for qv_kv_append, B rows.  Tokens on a page outside [0, num_pages) do not take part
  *               (a page may be given back once a window has left it behind).
  *   lens        [B] int32 tokens of each sequence, the new one included; cut to [0, max_pages * page_size].

@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 
 import bit_ptq_reconstruction_amd as qv  # noqa: E402
 from bit_ptq_reconstruction_amd.decode import QVKVCacheStruct  # noqa: E402
-from test_decode_abi import SHAPE, WORKSPACE, L  # noqa: E402,F401
+from test_decode_abi import SHAPE, UNSUPPORTED, WORKSPACE, L, gemv, linear  # noqa: E402,F401
 from test_decode_abi import append as abi_append, attend as abi_attend, heads as abi_heads  # noqa: E402
 from test_decode_binding import append, attend, bf, built, i32, refused  # noqa: E402,F401
 
@@ -71,3 +71,17 @@ def test_overlapping_outputs_of_the_library(L):
                 got = abi_attend(L, O=abi_heads(ts=ts, hs=hs), Q=abi_heads(ts=256), B=T, q_heads=H, size=0)
                 assert got == (SHAPE if bad else WORKSPACE), (T, H, ts, hs)
     assert abi_append(L, Q_out=abi_heads(ts=0)) == SHAPE and abi_append(L, Q_out=abi_heads(ts=64, hs=256)) == SHAPE
+
+
+def test_sizes_that_no_launch_holds(L):
+    """A launch holds fewer than 2^32 threads along a dimension: what passes that is refused before the first one."""
+    most = (1 << 29) - 64
+    assert gemv(L, N=most + 1, ldy=1 << 40) == UNSUPPORTED and linear(L, N=most + 1, ldy=1 << 40) == UNSUPPORTED
+    assert linear(L, N=most, ldy=1 << 40, work=None) == WORKSPACE
+    size = L.qv_paged_attention_workspace_size
+    short = dict(q_heads=4, pages=4)                          # 64 tokens: no join; two blocks of 256 threads a sequence
+    assert abi_attend(L, B=1 << 23, **short) == UNSUPPORTED and size(1 << 23, 4, 2, 64, 64) == 0
+    assert abi_attend(L, B=(1 << 23) - 1, work=None, **short) == WORKSPACE and size((1 << 23) - 1, 4, 2, 64, 64) == 256
+    long = dict(q_heads=32, pages=16, ld=16, O=abi_heads(ts=2048))  # 256 tokens: a join of 128 threads a query head
+    assert abi_attend(L, B=1 << 20, **long) == UNSUPPORTED and size(1 << 20, 32, 2, 64, 256) == 0
+    assert abi_attend(L, B=(1 << 20) - 1, work=None, **long) == WORKSPACE and size((1 << 20) - 1, 32, 2, 64, 256) > 256

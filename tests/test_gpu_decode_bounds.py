@@ -95,3 +95,20 @@ def test_single_row_of_any_stride(qv, dev, xt):
     assert bool(((Y[:1, :24].double().cpu() - y).abs() <= 1e-4).all())
     with pytest.raises(qv.QVError, match="ALIGN"):  # the next row is not aligned
         qv.qv_w4a16_gemv(wide[:2, :256], packed.to(dev), ws.to(dev), 128, None, Y[:2, :24])
+
+
+def test_rows_in_several_launches(qv, dev):
+    """More rows than one launch takes, against a call of the last of them alone."""
+    M, K, N, last = (1 << 20) + 45, 1024, 8, 61
+    g = gen(11)
+    q, packed, ws = random_weights(N, K, 128, g)
+    X = torch.randn((M, K), device=dev, dtype=torch.bfloat16)
+    Y = torch.full((M, N), float("nan"), device=dev)
+    work = torch.empty(qv.qv_w4a16_linear_workspace_size(M, K), dtype=torch.uint8, device=dev)
+    args = (None, packed.to(dev), ws.to(dev), 128, None)
+    qv.qv_w4a16_linear(X, *args, Y, work)
+    assert not bool(torch.isnan(Y).any())
+    for at in (0, (1 << 20) - 30, M - last):
+        few = torch.empty((last, N), device=dev)
+        qv.qv_w4a16_linear(X[at:at + last], *args, few, work)
+        assert torch.equal(few, Y[at:at + last])
