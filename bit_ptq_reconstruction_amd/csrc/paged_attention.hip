@@ -52,7 +52,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 4;  // of a block
-constexpr int kTile = 16;
+constexpr int kTile = (int)kTokensPerTile;
 constexpr int kCUs = 256, kMaxResident = 8;
 static_assert(kCUs * kMaxResident <= kManyBlocks, "a round of blocks");
 constexpr float kLog2e = 1.4426950408889634f;
@@ -113,20 +113,12 @@ struct Part {
 template <bool BY_PART>
 __device__ __forceinline__ Part find_part(const Args& a, int which) {
   const int lane = threadIdx.x & 63, B = (int)a.B;
-  // One round of blocks; more of them where each still has a long part (uneven lengths and starts even out).
-  const int least = (int)kMinTokensPerPart / kTile, enough = (int)kLongPart / kTile;
-  auto size_of_parts = [&](auto total, auto few, auto many) {
-    const int each = (int)((total + few - 1) / few), at_most = (int)((total + many - 1) / many);
-    const int more = at_most > enough ? at_most : enough;
-    const int per = each < more ? each : more;
-    return __builtin_amdgcn_readfirstlane(per < least ? least : per);
-  };
   Part p;
   const int mine = lane < B ? a.lens[lane] : 0;  // of the first 64 sequences
   const Span own = span_of(a, mine);
   if (B <= 64 && a.few_tiles) {  // the totals fit 32 bits
     const uint32_t total = __builtin_amdgcn_readlane(scan(own.last - own.first), 63);
-    p.per_part = size_of_parts(total, (uint32_t)a.few, (uint32_t)a.many);
+    p.per_part = __builtin_amdgcn_readfirstlane(tiles_of_part(total, (uint32_t)a.few, (uint32_t)a.many));
   } else {
     uint64_t total = own.last - own.first;
     for (int i = lane + 64; i < B; i += 64) {
@@ -135,7 +127,7 @@ __device__ __forceinline__ Part find_part(const Args& a, int which) {
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-    p.per_part = size_of_parts(total, (uint64_t)a.few, (uint64_t)a.many);
+    p.per_part = __builtin_amdgcn_readfirstlane(tiles_of_part(total, (uint64_t)a.few, (uint64_t)a.many));
   }
   int base = 0;  // parts of the sequences before
   p.b = -1;

@@ -65,6 +65,17 @@ constexpr int64_t kQueriesPerBlock = 16;    // query heads of one cache head tha
 constexpr int64_t kMinTokensPerPart = 128;  // a unit of work for each wave of a block
 constexpr int64_t kLongPart = 1536;         // tokens from which a block's start no longer counts
 constexpr int64_t kManyBlocks = 4096;       // no less than a round of them
+constexpr int64_t kTokensPerTile = 16;
+// Tiles of a part where all sequences together have `total`: one round of blocks (`few` parts), or more of them where each
+// still has a long part (uneven lengths and starts even out), `many` at most.  No sequence has more than 2^27 tiles.
+template <typename U>
+constexpr int tiles_of_part(U total, U few, U many) {
+  const U each = (total + few - 1) / few, at_most = (total + many - 1) / many;
+  const U least = kMinTokensPerPart / kTokensPerTile, enough = kLongPart / kTokensPerTile, all = U{1} << 27;
+  const U more = at_most > enough ? at_most : enough;
+  const U per = each < more ? each : more;
+  return (int)(per < least ? least : (per > all ? all : per));
+}
 struct AttentionParts {
   int64_t many, most;
   int64_t blocks;  // of a part

@@ -1,5 +1,8 @@
 """Further calls that the single-token entry points refuse on the host (CPU only: nothing reaches the GPU)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 
@@ -7,7 +10,7 @@ torch = pytest.importorskip("torch")
 
 import bit_ptq_reconstruction_amd as qv  # noqa: E402
 from bit_ptq_reconstruction_amd.decode import QVKVCacheStruct  # noqa: E402
-from test_decode_abi import SHAPE, UNSUPPORTED, WORKSPACE, L, gemv, linear  # noqa: E402,F401
+from test_decode_abi import ROOT, SHAPE, UNSUPPORTED, WORKSPACE, L, gemv, linear  # noqa: E402,F401
 from test_decode_abi import append as abi_append, attend as abi_attend, heads as abi_heads  # noqa: E402
 from test_decode_binding import append, attend, bf, built, i32, refused  # noqa: E402,F401
 
@@ -85,3 +88,15 @@ def test_sizes_that_no_launch_holds(L):
     long = dict(q_heads=32, pages=16, ld=16, O=abi_heads(ts=2048))  # 256 tokens: a join of 128 threads a query head
     assert abi_attend(L, B=1 << 20, **long) == UNSUPPORTED and size(1 << 20, 32, 2, 64, 256) == 0
     assert abi_attend(L, B=(1 << 20) - 1, work=None, **long) == WORKSPACE and size((1 << 20) - 1, 32, 2, 64, 256) > 256
+
+
+def test_parts_of_any_batch_have_room(tmp_path):
+    """The attention's cut into parts against the room that the workspace has for them."""
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    stubs, exe = os.path.join(ROOT, "tests", "sanitize"), str(tmp_path / "parts_check")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", stubs, "-I",
+                    os.path.join(ROOT, "include"), "-I", os.path.join(ROOT, "bit_ptq_reconstruction_amd", "csrc"),
+                    os.path.join(stubs, "parts_check.cpp"), "-o", exe], check=True, capture_output=True, text=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
