@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_decode import DT, U, attend, codes32, dev, fill, gen, make_cache, qv, shuffled_table  # noqa: E402,F401
+from test_gpu_decode import DT, U, attend, attention64, check_attention, codes32, dev, fill, gen, make_cache, qv, shuffled_table  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,19 @@ def test_int8_append_of_what_is_not_finite(qv, dev, xt, dim):
     Q = torch.randn((1, 3, dim), generator=g).to(DT[xt]).to(dev)
     n = lambda *lens: torch.isnan(attend(qv, dev, Q, cache, table, list(lens)).float()).all(2).tolist()
     assert n(3) == [[False, False, False]] and n(4) == [[False, True, False]] and n(20) == [[True, True, True]]
+
+
+@pytest.mark.parametrize("xt,kind,dim,heads,share", [("bf16", "bf16", 128, 8, 4), ("bf16", "bf16", 64, 16, 1), ("fp32", "int8", 128, 5, 8),
+                                                     ("bf16", "int8", 128, 8, 4), ("fp32", "bf16", 128, 20, 2)])
+def test_join_of_many_heads(qv, dev, xt, kind, dim, heads, share):
+    """More than 512 query heads in all, over sequences of many parts, of one and of none."""
+    g = gen(dim + heads)
+    lens = ([2500, 0, 1, 700, 128, 1900, 129, 33, 16, 1000] * 4)[:512 // (heads * share) + 1]
+    table, pages = shuffled_table(lens, 16, g)
+    cache = make_cache(qv, dev, pages, heads, 16, dim, kind, 0)
+    kv = fill(cache, table, lens, g)
+    Q = torch.randn((len(lens), heads * share, dim), generator=g).to(DT[xt])
+    O = attend(qv, dev, Q.to(dev), cache, table.to(dev), lens)
+    o, mag = attention64(Q, kv, lens, 0, dim ** -0.5)
+    check_attention(O, o, mag, xt, f"{len(lens)} sequences")
+    assert bool((O[[n == 0 for n in lens]] == 0).all())

@@ -10,6 +10,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from guard import check_guard, guarded_output  # noqa: E402
 from test_gpu_decode import BF, DT, U, dev, gen, hadamard64, qv, random_weights  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
@@ -112,3 +113,48 @@ def test_rows_in_several_launches(qv, dev):
         few = torch.empty((last, N), device=dev)
         qv.qv_w4a16_linear(X[at:at + last], *args, few, work)
         assert torch.equal(few, Y[at:at + last])
+
+
+@pytest.mark.parametrize("M,K,N,group,xt,yt", [
+    (2, 4096, 1500, 128, "bf16", "bf16"), (2, 4096, 3000, 256, "bf16", "bf16"), (4, 4096, 2000, 512, "fp32", "fp32"),
+    (3, 4096, 4000, 128, "fp32", "fp32"), (5, 4096, 8300, 128, "bf16", "bf16"), (5, 4096, 9001, 512, "fp32", "fp32"),
+    (2, 4096, 17000, 4096, "bf16", "fp32"), (1, 4096, 6000, 128, "fp32", "bf16"), (12, 1024, 9000, 128, "bf16", "bf16"),
+    (11, 1024, 8201, 1024, "fp32", "fp32"), (7, 1024, 5000, 256, "fp32", "bf16"), (1, 1024, 17000, 128, "bf16", "fp32"),
+    (13, 1024, 9000, 128, "bf16", "bf16"), (6, 4096, 9000, 128, "bf16", "fp32"), (2, 4096, 9000, 128, "bf16", "bf16"),
+    (3, 4096, 1000, 256, "fp32", "bf16"),
+])
+def test_wide_rotated_layers(qv, dev, M, K, N, group, xt, yt):
+    """Rotated rows with every number of channels to a block.  The rotation adds log2 K roundings to an activation, each of u of
+    the row's norm over sqrt K at the most in the root of their squares: 12 u |x| / sqrt K |s q| in the whole."""
+    check_wide(qv, dev, M, K, N, group, xt, yt, True)
+
+
+@pytest.mark.parametrize("M,K,N,group,xt,yt", [
+    (3, 1152, 9001, 128, "fp32", "fp32"), (16, 2048, 9000, 512, "fp32", "fp32"), (1, 4096, 8300, 128, "fp32", "bf16"),
+    (31, 2048, 2000, 128, "bf16", "fp32"), (40, 1024, 3000, 256, "bf16", "bf16"), (100, 512, 12000, 128, "bf16", "bf16"),
+    (20, 4096, 9000, 4096, "fp32", "fp32"), (2, 2176, 1030, 128, "bf16", "bf16"), (2, 4224, 1000, 128, "fp32", "bf16"),
+])
+def test_wide_layers(qv, dev, M, K, N, group, xt, yt):
+    """Rows out of memory with every number of channels and row tiles to a block."""
+    check_wide(qv, dev, M, K, N, group, xt, yt, False)
+
+
+def check_wide(qv, dev, M, K, N, group, xt, yt, rotate):
+    """An fp32 sum of K exact products errs like a random walk of them: 8 deviations of sqrt(K) u |s x q| in an element."""
+    g = gen(M + K + N)
+    q, packed, ws = random_weights(N, K, group, g)
+    X = torch.randn((M, K), generator=g).to(DT[xt])
+    work = torch.empty(qv.qv_w4a16_linear_workspace_size(M, K), dtype=torch.uint8, device=dev)
+    full, Y = guarded_output(M, N, DT[yt], dev, 5)
+    if rotate:
+        qv.qv_w4a16_linear(X.to(dev), None, packed.to(dev), ws.to(dev), group, None, Y, work)
+    else:
+        qv.qv_w4a16_gemv(X.to(dev), packed.to(dev), ws.to(dev), group, None, Y)
+    check_guard(full, M, N)
+    x = X.double() @ hadamard64(K) / math.sqrt(K) if rotate else X.double()
+    w = q.double() * ws.double().repeat_interleave(group, 1)
+    y, norm = x @ w.t(), ((x ** 2) @ (w.t() ** 2)).sqrt()
+    extra = 12 * U * (x.norm(dim=1, keepdim=True) / math.sqrt(K)) * w.norm(dim=1) if rotate else 0.0
+    tol = 8 * (math.sqrt(K) * U * norm + extra) + (BF * 1.01 * y.abs() if yt == "bf16" else U * y.abs())
+    worst = ((Y.double().cpu() - y).abs() / tol).max().item()
+    assert worst <= 1.0, f"{worst:.2f} of the bound"
