@@ -158,3 +158,21 @@ def check_wide(qv, dev, M, K, N, group, xt, yt, rotate):
     tol = 8 * (math.sqrt(K) * U * norm + extra) + (BF * 1.01 * y.abs() if yt == "bf16" else U * y.abs())
     worst = ((Y.double().cpu() - y).abs() / tol).max().item()
     assert worst <= 1.0, f"{worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("M,K,N,group,xt,rotate", [
+    (4, 1024, 1000, 128, "bf16", False), (16, 4096, 3000, 512, "fp32", False), (3, 4096, 1024, 128, "bf16", True),
+    (40, 2048, 4100, 128, "bf16", False), (12, 1024, 2000, 1024, "fp32", True), (1, 8192, 700, 256, "bf16", False),
+])
+def test_whole_fp32_results(qv, dev, M, K, N, group, xt, rotate):
+    """The 2-norm of all errors over that of |s x q|.  Up to 384 additions of a window's exact products at partial sums that
+    grow to its norm: the root of 384 / 2 times u / sqrt 3, 8 u; then K / 128 + 8 sums of windows and waves (72 / 2: 3.5 u); the
+    rotation's log2 K roundings of an activation (2 u).  The root of their squares is below 10 u."""
+    g = gen(M * 31 + N)
+    q, _, ws = random_weights(N, K, group, g)
+    X = torch.randn((M, K), generator=g).to(DT[xt])
+    Y = linear(qv, dev, X, q, ws, group, rotate, "fp32")
+    x = X.double() @ hadamard64(K) / math.sqrt(K) if rotate else X.double()
+    w = q.double() * ws.double().repeat_interleave(group, 1)
+    off = ((Y - x @ w.t()).norm() / ((x ** 2) @ (w.t() ** 2)).sqrt().norm()).item()
+    assert off <= 10 * U, f"{off / U:.1f} u"
