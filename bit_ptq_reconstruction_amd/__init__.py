@@ -29,7 +29,7 @@ _DECODE = frozenset(__all__[__all__.index("qv_w4a16_gemv"):])
 
 
 def __getattr__(name: str):
-    """The single-token entry points come with torch, which this module itself imports only when it is used."""
+    """The single-token entry points."""
     if name in _DECODE:
         from . import decode
 

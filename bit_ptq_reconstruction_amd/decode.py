@@ -10,8 +10,6 @@ from __future__ import annotations
 
 import ctypes
 
-import torch  # noqa: F401  (the extension module links against it)
-
 from . import QV_EPI_NONE, lib
 
 __all__ = [
@@ -68,6 +66,8 @@ class _Unloaded:
         global _native
         lib()  # libqv.so, or its ImportError
         try:
+            import torch  # noqa: F401  (the extension module links against it)
+
             from . import _decode
         except ImportError as e:
             raise ImportError(f"{e}; the extension module _decode.so is built by __graft_entry__.build()") from e

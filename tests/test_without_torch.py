@@ -40,3 +40,12 @@ else:
     assert False
 assert os.path.exists(build.LIB) and not os.path.exists(build.BINDING)
 """, str(tmp_path))
+
+
+def test_package_imports():
+    """Every public name, the single-token calls among them; those need torch when they are called."""
+    run("""
+from bit_ptq_reconstruction_amd import *
+import bit_ptq_reconstruction_amd as qv
+assert qv_paged_attention is qv.qv_paged_attention and QV_KV_INT8 == 1 and callable(qv_w4a4_gemm)
+""")
