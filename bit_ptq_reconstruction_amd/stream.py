@@ -17,8 +17,8 @@ GROUP = 128
 class StreamBlock:
     """``weights``: {"qkv", "proj", "fc1", "fc2"} -> [N, K] fp32/bf16 of a block of width 1024 with ``heads`` heads.
 
-    Buffers for ``sequences`` sequences of up to ``capacity`` tokens are allocated here and nothing later, so a step
-    can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle."""
+    Buffers for ``sequences`` sequences of up to ``capacity`` tokens (rounded up to whole pages) are allocated here and
+    nothing later, so a step can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle."""
 
     def __init__(self, qv, weights, sequences: int, capacity: int, device, heads: int = 16, axes: int = 1,
                  positions: int = 4096, base: float = 10000.0, int8_cache: bool = False, page_size: int = 64,
@@ -43,6 +43,7 @@ class StreamBlock:
                                   torch.zeros(shape, dtype=kind, device=device), *scales)
         self.table = torch.arange(sequences * pages, dtype=torch.int32, device=device).view(sequences, pages)
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
+        self.held = [0] * sequences  # the host's copy of lens
         self.position = torch.zeros((sequences, axes), dtype=torch.int32, device=device)
         w = self.dim // axes
         angle = torch.arange(positions, device=device)[:, None] * base ** (-torch.arange(0, w, 2, device=device) / w)
@@ -69,6 +70,18 @@ class StreamBlock:
             qv.qv_w4a4_linear_grouped(x, None, GROUP, self.Wq[name], self.ws[name], None, b[name], b["work"], lin.epi)
         return b[name]
 
+    def _need_room(self, tokens: int, sequences) -> None:
+        room = self.table.shape[1] * self.cache.page_size
+        for s in sequences:
+            if self.held[s] + tokens > room:
+                raise ValueError(f"StreamBlock: sequence {s} holds {self.held[s]} tokens and has no room for {tokens} more in {room}")
+
+    def reserve(self) -> None:
+        """Counts one token of every sequence, or raises ValueError where one has no room: to be called before each replay
+        of a captured step, which the host does not see.  (Who sets ``lens`` sets ``held`` as well.)"""
+        self._need_room(1, range(self.B))
+        self.held = [n + 1 for n in self.held]
+
     def _norm(self, x):
         import torch
 
@@ -84,18 +97,28 @@ class StreamBlock:
         import torch
 
         T, b = x.shape[0], self.frame
+        self._need_room(T, [sequence])
         q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=False))
         index = self.lens[sequence] + torch.arange(T, dtype=torch.int32, device=x.device)
         owner = torch.full_like(index, sequence)
         self.qv.qv_kv_append(self.cache, self.table, owner, index, k, v, self.cos, self.sin, position)
         self.lens[sequence] += T
+        self.held[sequence] += T
 
     def step(self, x):
-        """One new token x [B, 1024] bf16 of every sequence, at ``self.position`` [B, axes]; returns the block's output."""
+        """One new token x [B, 1024] bf16 of every sequence, at ``self.position`` [B, axes]; returns the block's output.
+        ValueError where a sequence has no room for it."""
+        import torch
+
         qv, b = self.qv, self.one
+        captured = torch.cuda.is_current_stream_capturing()  # runs later, see reserve()
+        if not captured:
+            self._need_room(1, range(self.B))
         q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=True))
         qv.qv_kv_append(self.cache, self.table, None, self.lens, k, v, self.cos, self.sin, self.position, q, b["q"])
         self.lens += 1
+        if not captured:
+            self.held = [n + 1 for n in self.held]
         qv.qv_paged_attention(b["q"], self.cache, self.table, self.lens, b["o"], b["parts"])
         y = x + self._linear("proj", b["o"].view(self.B, self.width), b, few=True)
         return y + self._linear("fc2", self._linear("fc1", self._norm(y), b, few=True), b, few=True)

@@ -50,6 +50,7 @@ def main(argv=None):
     torch.cuda.synchronize()
     t = time.perf_counter()
     for _ in range(a.tokens):
+        block.reserve()
         graph.replay()
     torch.cuda.synchronize()
     us = (time.perf_counter() - t) / a.tokens * 1e6
