@@ -154,10 +154,10 @@ qv_status qv_kv_append(const qv_kv_cache* cache, const int32_t* page_table, int6
     if (!token_seq && T > num_seqs) return QV_ERR_SHAPE;
     if (axes != 1 && axes != 2) return QV_ERR_UNSUPPORTED;
     if (places < 0 || places > kMaxInt) return QV_ERR_SHAPE;
-    if (!cos != !sin || (cos && !position && axes != 1)) return QV_ERR_NULL;
+    if (!cos != !sin) return QV_ERR_NULL;
     if ((Q == nullptr) != (Q_out == nullptr) || (Q == nullptr) != (q_heads == 0)) return QV_ERR_NULL;
     if (T == 0) return QV_OK;
-    if (!K || !V || !token_index) return QV_ERR_NULL;
+    if (!K || !V || !token_index || (cos && !position && axes != 1)) return QV_ERR_NULL;
     if (!aligned(token_seq, 4) || !aligned(token_index, 4) || !aligned(position, 4) || !aligned(cos) || !aligned(sin))
       return QV_ERR_ALIGN;
     const qv_heads* rows[] = {K, V, Q, Q_out};

@@ -100,3 +100,8 @@ def test_parts_of_any_batch_have_room(tmp_path):
                     os.path.join(stubs, "parts_check.cpp"), "-o", exe], check=True, capture_output=True, text=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_append_of_no_tokens(L):
+    """No tokens, no positions: accepted with two axes as well."""
+    assert abi_append(L, T=0, axes=2, position=None) == 0 and abi_append(L, T=1, axes=2, position=None) == 1

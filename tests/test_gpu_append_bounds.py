@@ -57,3 +57,12 @@ def test_long_appends(qv, dev, T, heads, q_heads, dim, axes, xt, kind, rotate):
             assert int((~torch.isnan(scales)).sum()) == T * heads
     if Q is not None:
         assert torch.equal(out[:T].cpu(), turned(Q).to(DT[xt])) and bool(torch.isnan(out[T:].float()).all())
+
+
+def test_append_of_no_tokens_on_two_axes(qv, dev):
+    """An empty run of tokens, whose empty tensors have no address, is a call like any other."""
+    cache = make_cache(qv, dev, 2, 2, 16, 64, "bf16", 0)
+    e = lambda *s: torch.empty(s, device=dev)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+    qv.qv_kv_append(cache, i(1, 2), i(0), i(0), e(0, 2, 64), e(0, 2, 64), e(9, 16), e(9, 16), i(0, 2), e(0, 4, 64), e(0, 4, 64))
+    assert bool(torch.isnan(cache.k_pages).all())
