@@ -18,7 +18,8 @@ class StreamBlock:
     """``weights``: {"qkv", "proj", "fc1", "fc2"} -> [N, K] fp32/bf16 of a block of width 1024 with ``heads`` heads.
 
     Buffers for ``sequences`` sequences of up to ``capacity`` tokens (rounded up to whole pages) are allocated here and
-    nothing later, so a step can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle."""
+    nothing later, so a step can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle.
+    A frame has up to ``frame_tokens`` tokens."""
 
     def __init__(self, qv, weights, sequences: int, capacity: int, device, heads: int = 16, axes: int = 1,
                  positions: int = 4096, base: float = 10000.0, int8_cache: bool = False, page_size: int = 64,
@@ -49,7 +50,7 @@ class StreamBlock:
         angle = torch.arange(positions, device=device)[:, None] * base ** (-torch.arange(0, w, 2, device=device) / w)
         self.cos, self.sin = angle.cos(), angle.sin()
         self.one = self._buffers(sequences, empty, byte, few=True)
-        self.frame = self._buffers(frame_tokens, empty, byte, few=False) if frame_tokens else None
+        self.frame = self._buffers(frame_tokens, empty, byte, few=False)
 
     def _buffers(self, rows, empty, byte, few: bool):
         qv = self.qv
@@ -96,7 +97,11 @@ class StreamBlock:
         inside a frame is not part of this class."""
         import torch
 
-        T, b = x.shape[0], self.frame
+        T, b = x.shape[0], {name: t[:x.shape[0]] if name in self.linears else t for name, t in self.frame.items()}
+        if not 0 <= sequence < self.B:
+            raise ValueError(f"StreamBlock: sequence {sequence} of {self.B}")
+        if T > len(self.frame["qkv"]):
+            raise ValueError(f"StreamBlock: a frame of {T} tokens, the block was made for frames of up to {len(self.frame['qkv'])}")
         self._need_room(T, [sequence])
         q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=False))
         index = self.lens[sequence] + torch.arange(T, dtype=torch.int32, device=x.device)

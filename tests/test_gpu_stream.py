@@ -3,7 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_decode import dev, gen, qv, turn32  # noqa: E402,F401
+from test_gpu_decode import codes32, dev, gen, qv, turn32  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,45 @@ def test_no_room(qv, dev, weights):
             call()
     assert block.lens.tolist() == block.held == [2, 32]
     assert torch.equal(before.view(torch.int16), block.cache.k_pages.view(torch.int16))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_frames_of_any_size(qv, dev, weights, int8):
+    """Frames up to ``frame_tokens``: what they store, against the linear's own output turned by position; larger ones, and
+    frames of a block that was made for none, are refused."""
+    from bit_ptq_reconstruction_amd.stream import GROUP
+
+    g = gen(3)
+    block = make(qv, dev, weights, capacity=64, int8_cache=int8)
+    expect = [[], []]
+    for sequence, T in ((1, 30), (0, 7), (1, 1), (1, 13), (0, 0)):
+        x, at = rows(T, g, dev), places(T, g, dev)
+        block.take_frame(x, sequence, at)
+        if T == 0:
+            continue
+        qkv = torch.empty((T, 3072), dtype=torch.bfloat16, device=dev)
+        work = torch.empty(qv.qv_w4a4_linear_grouped_workspace_size(T, 1024, GROUP), dtype=torch.uint8, device=dev)
+        qv.qv_w4a4_linear_grouped(torch.nn.functional.layer_norm(x, (1024,)), None, GROUP, block.Wq["qkv"], block.ws["qkv"],
+                                  None, qkv, work)
+        qkv = qkv.cpu().view(T, 3, 16, 64)
+        expect[sequence].append((turn32(qkv[:, 1], block.cos.cpu(), block.sin.cpu(), at.cpu(), 2), qkv[:, 2].float()))
+    assert block.lens.tolist() == block.held == [7, 44]
+    for s in range(2):
+        t = torch.arange(block.held[s])
+        page, slot = block.table[s].cpu().long()[t // 16], t % 16
+        for i, (pages, scales) in enumerate(((block.cache.k_pages, block.cache.k_scale), (block.cache.v_pages, block.cache.v_scale))):
+            x = torch.cat([e[i] for e in expect[s]])
+            got = pages.cpu()[page, :, slot]
+            if int8:
+                codes, scale = codes32(x)
+                assert torch.equal(got, codes) and torch.equal(scales.cpu()[page, :, slot], scale)
+            else:
+                assert torch.equal(got, x.to(torch.bfloat16))
+    with pytest.raises(ValueError, match="a frame of 31 tokens, the block was made for frames of up to 30"):
+        block.take_frame(rows(31, g, dev), 0, places(31, g, dev))
+    with pytest.raises(ValueError, match="sequence 2 of 2"):
+        block.take_frame(rows(1, g, dev), 2, places(1, g, dev))
+    none = make(qv, dev, weights, frame_tokens=0)
+    with pytest.raises(ValueError, match="a frame of 5 tokens, the block was made for frames of up to 0"):
+        none.take_frame(rows(5, g, dev), 0, places(5, g, dev))
+    assert block.held == [7, 44] and none.held == [0, 0]
