@@ -27,6 +27,8 @@ class StreamBlock:
         import torch
 
         self.qv, self.B, self.heads, self.width = qv, sequences, heads, 1024
+        if heads not in (8, 16):
+            raise ValueError(f"StreamBlock: {heads} heads of a width of 1024, the attention takes 64 (16 heads) or 128 (8) channels")
         self.dim = self.width // heads
         empty = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=device)
         byte = lambda n: empty(n, dtype=torch.uint8)

@@ -94,3 +94,11 @@ def test_frames_of_any_size(qv, dev, weights, int8):
     with pytest.raises(ValueError, match="a frame of 5 tokens, the block was made for frames of up to 0"):
         none.take_frame(rows(5, g, dev), 0, places(5, g, dev))
     assert block.held == [7, 44] and none.held == [0, 0]
+
+
+def test_eight_heads(qv, dev, weights):
+    """The other number of heads that the attention takes."""
+    g = gen(6)
+    block = make(qv, dev, weights, heads=8)
+    block.take_frame(rows(9, g, dev), 0, places(9, g, dev))
+    assert bool(torch.isfinite(block.step(rows(2, g, dev)).float()).all()) and block.lens.tolist() == [10, 1]
