@@ -18,7 +18,8 @@ class StreamBlock:
     """``weights``: {"qkv", "proj", "fc1", "fc2"} -> [N, K] fp32/bf16 of a block of width 1024 with ``heads`` heads.
 
     Buffers for ``sequences`` sequences of up to ``capacity`` tokens (rounded up to whole pages) are allocated here and
-    nothing later, so a step can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle.
+    nothing later, so a step can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle;
+    the output of a token at another one, and of those that come after it in its sequence, is NaN.
     A frame has up to ``frame_tokens`` tokens."""
 
     def __init__(self, qv, weights, sequences: int, capacity: int, device, heads: int = 16, axes: int = 1,
@@ -41,9 +42,11 @@ class StreamBlock:
         pages = -(-capacity // page_size)
         shape = (sequences * pages, heads, page_size, self.dim)
         kind = torch.int8 if int8_cache else torch.bfloat16
-        scales = [torch.zeros(shape[:3], device=device) for _ in range(2)] if int8_cache else [None, None]
-        self.cache = qv.QVKVCache(torch.zeros(shape, dtype=kind, device=device),
-                                  torch.zeros(shape, dtype=kind, device=device), *scales)
+        # NaN (int8: under scales of NaN), so that a token that was not stored shows in whatever attends to it.
+        nan = float("nan")
+        scales = [torch.full(shape[:3], nan, device=device) for _ in range(2)] if int8_cache else [None, None]
+        self.cache = qv.QVKVCache(*(torch.full(shape, 0 if int8_cache else nan, dtype=kind, device=device) for _ in range(2)),
+                                  *scales)
         self.table = torch.arange(sequences * pages, dtype=torch.int32, device=device).view(sequences, pages)
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
         self.held = [0] * sequences  # the host's copy of lens

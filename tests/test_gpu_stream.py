@@ -102,3 +102,29 @@ def test_eight_heads(qv, dev, weights):
     block = make(qv, dev, weights, heads=8)
     block.take_frame(rows(9, g, dev), 0, places(9, g, dev))
     assert bool(torch.isfinite(block.step(rows(2, g, dev)).float()).all()) and block.lens.tolist() == [10, 1]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_position_outside(qv, dev, weights, int8):
+    """A position without an angle shows as NaN in its sequence, then and in the steps behind it, whose past lacks the token; the
+    other sequence is untouched."""
+    g = gen(5)
+    frame, at = rows(20, g, dev), places(20, g, dev)
+    x = [rows(2, g, dev) for _ in range(3)]
+    p = [places(2, g, dev) for _ in range(3)]
+    outs = []
+    for bad in (False, True):
+        block = make(qv, dev, weights, int8_cache=int8)
+        for s in range(2):
+            block.take_frame(frame, s, at)
+        got = []
+        for i in range(3):
+            block.position.copy_(p[i])
+            if bad and i == 1:
+                block.position[0, 1] = 40
+            got.append(block.step(x[i]).float().cpu())
+        outs.append(got)
+    clean, spoilt = outs
+    assert torch.equal(spoilt[0], clean[0])
+    for i in (1, 2):
+        assert bool(torch.isnan(spoilt[i][0]).all()) and torch.equal(spoilt[i][1], clean[i][1])
