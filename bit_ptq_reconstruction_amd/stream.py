@@ -17,8 +17,11 @@ GROUP = 128
 class StreamBlock:
     """``weights``: {"qkv", "proj", "fc1", "fc2"} -> [N, K] fp32/bf16 of a block of width 1024 with ``heads`` heads.
 
-    Buffers for ``sequences`` sequences of up to ``capacity`` tokens (rounded up to whole pages) are allocated here and
-    nothing later, so a step can be captured in a graph.  ``positions`` places along each of ``axes`` axes have an angle;
+    The block has no biases, no weights in its norms and no smoothing.
+
+    The cache for ``sequences`` sequences of up to ``capacity`` tokens (rounded up to whole pages), the workspaces and the
+    linears' and the attention's outputs are allocated here, so a step can be captured in a graph.  The norms and residual
+    sums are torch's and allocate theirs (under capture from the graph's pool), and so does take_frame().  ``positions`` places along each of ``axes`` axes have an angle;
     the output of a token at another one, and of those that come after it in its sequence, is NaN.
     A frame has up to ``frame_tokens`` tokens."""
 
