@@ -31,8 +31,12 @@
 //   channels 5.8, 4 channels 5.3; fp32, one rotated row 8.3 and 7.4.
 // Rows beyond 16 count as blocks in that; where 16 to a block would take several rounds, bf16 rows go 32 to a block, which
 // then unpacks each code for both halves: 32 rows x 4096 x 16384 in 22.8 and 15.8 us, 4096 x 4000 in 9.8 and 8.3.
-// Rows are rotated by every block for itself, or by a kernel before (us, N = 1024): K = 1024, one row 4.5 and 5.9, 12 rows
-// 6.0 and 6.4, 16 rows 6.8 and 6.5; K = 4096, one row 6.2 and 9.5, 5 rows 9.0 and 9.6, 6 rows 9.7 and 9.1.
+// Rows are rotated by every block for itself, or by a kernel before.  Where blocks take turns on a CU, each rotates the rows
+// again, so the rule goes by rounds of blocks as well (us, rotated in the block and before, bf16 rows):
+//   K = 1024, 1 and 12 rows    N = 1024 4.6, 5.8 and 6.3, 6.4    16384 (one round) 7.1, 8.5 and 9.3, 9.9    32768 15.5, 14.9 and 18.3, 16.2
+//   K = 4096, N = 1024         1 row 5.8, 9.1    5 rows 9.4, 9.7
+//             N = 32768        1 row 27.9, 30.7    3 rows 30.8, 31.6    4 rows 32.2, 31.7
+//             N = 65536        1 row 56.4, 60.1    2 rows 59.4, 60.6    3 rows 62.1, 61.0
 #include <hip/hip_bf16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -639,8 +643,9 @@ hipError_t by_types(const Args<X>& a, hipStream_t st) {
 template <typename X>
 hipError_t launch(const Args<X>& a, bool rotate, float* rows32, hipStream_t st) {
   if (!rotate) return by_types<X, kStaged>(a, st);
-  if (a.K == 1024 && a.M <= kFused1024) return by_types<X, kRot1024>(a, st);
-  if (a.K == 4096 && a.M <= kFused4096) return by_types<X, kRot4096>(a, st);
+  const int64_t rounds = (a.N + 64 * kCUs - 1) / (64 * kCUs);  // of blocks of 64 channels
+  const int64_t fused = a.K == 1024 ? (rounds == 1 ? kFused1024 : 0) : (rounds == 1 ? kFused4096 : (rounds == 2 ? 3 : 2));
+  if (a.M <= fused) return a.K == 1024 ? by_types<X, kRot1024>(a, st) : by_types<X, kRot4096>(a, st);
   constexpr int64_t kStep = int64_t{1} << 20;  // rows of a launch, which holds fewer than 2^32 threads
   for (int64_t m = 0; m < a.M; m += kStep) {
     const unsigned rows = (unsigned)(a.M - m < kStep ? a.M - m : kStep);

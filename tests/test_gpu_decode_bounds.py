@@ -176,3 +176,10 @@ def test_whole_fp32_results(qv, dev, M, K, N, group, xt, rotate):
     w = q.double() * ws.double().repeat_interleave(group, 1)
     off = ((Y - x @ w.t()).norm() / ((x ** 2) @ (w.t() ** 2)).sqrt().norm()).item()
     assert off <= 10 * U, f"{off / U:.1f} u"
+
+
+@pytest.mark.parametrize("M,K,N,xt,yt", [(1, 1024, 16450, "bf16", "bf16"), (12, 1024, 16385, "fp32", "bf16"), (3, 4096, 16391, "bf16", "bf16"),
+                                         (4, 4096, 16390, "bf16", "fp32"), (2, 4096, 33000, "fp32", "fp32")])
+def test_rotated_layers_of_several_rounds(qv, dev, M, K, N, xt, yt):
+    """More channels than one round of blocks takes, where rows are rotated by a kernel before from fewer rows on."""
+    check_wide(qv, dev, M, K, N, 128, xt, yt, True)
