@@ -4,10 +4,13 @@
 //   O[b][i] = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q_i . k_t - m),  m the running maximum
 //
 // One pass over the keys and values, which is all there is to move: the kernel is bound by memory.  48 sequences of up to
-// 16384 tokens (8 heads of 128, 32 queries, 1.6 GB) take 270 us, 6.0 TB/s (a copy runs at 5.0; the matrix cores are busy for 6 %
-// and the vector ALU for 13 % of the time); two of 99991 tokens in int8 (211 MB) take 47-48 us, 4.4 TB/s (vector ALU
-// 43 %, for the conversions).  One frame of 1374 tokens (5.6 MB) takes 7.9 us: 5.0 for the parts' chain of loads (lengths,
+// 16384 tokens (8 heads of 128, 32 queries, 1.6 GB) take 270 us, 6.0 TB/s (a copy runs at 5.0; the matrix cores are busy for 8 %
+// and the vector ALU for 14 % of the time); two of 99991 tokens in int8 (211 MB) take 49-50 us, 4.3 TB/s (vector ALU
+// 44 %, for the conversions).  One frame of 1374 tokens (5.6 MB) takes 7.9 us: 5.0 for the parts' chain of loads (lengths,
 // page table, keys) and 2.9 for the join.
+// Every block finds its part from the lengths of all sequences, which tells from many short ones on: 256 sequences of 1374 tokens
+// (16 heads of 64) run at 6.1 TB/s, 1024 of 100 tokens (8 heads of 128, 32 queries) take 181 us, 2.4 TB/s, and 4096 of 64 tokens
+// 1447 us, 0.8 TB/s.
 //
 // A wave takes two tiles of 16 tokens at a time and the up to 16 query heads that share a cache head, and nothing leaves its
 // registers between the two products:
@@ -15,9 +18,9 @@
 //                   the scores of tokens 4 c + i (i < 4) for query r.
 //   O^T += V^T P^T  over 32 tokens, slots 8 c + 4 u + i being token 4 c + i of tile u: so a lane's own scores are its operand,
 //                   in three bf16 pieces that sum to them (two would leave up to 2^-15 of each, always of its sign, while the
-//                   sum that divides the result takes it whole).  The other operand is value channel D / 16 r + e of the same tokens: each lane
-//                   loads D / 16 neighbouring channels of four tokens a tile and picks channel e of a pair of tokens with one
-//                   byte permutation.  The result has query r in lane (r, c), channels 4 D / 16 c onwards, next
+//                   sum that divides the result takes it whole).  The other operand is value channel D / 16 r + e of the
+//                   same tokens: each lane loads D / 16 neighbouring channels of four tokens a tile and picks channel e of a
+//                   pair of tokens with one byte permutation.  The result has query r in lane (r, c), channels 4 D / 16 c onwards, next
 //                   to that query's maximum and sum.
 // Both are v_mfma_f32_16x16x32_bf16.  The order of channels inside S and of tokens inside O is free, which is what makes the
 // loads contiguous and saves any exchange between lanes.  (v_mfma_f32_16x16x4_f32 takes P unrounded and needs no pieces, but

@@ -5,9 +5,9 @@
 //
 // With a few rows the weights' N K / 2 bytes are all there is to move.  Small layers are bound by latency (a 1024 x
 // 1024 layer takes 3.1 us unrotated and 4.5 us rotated for one row, in a graph whose empty nodes take about 2.5), large
-// ones by the cache-line requests of a CU: 16 rows x 8192 x 16384 take 19-21 us, 72 MB at 3.5-3.7 TB/s (a copy's rate, 5.0
-// TB/s, would be 14.4 us and the launch).  There, without the scales' loads the kernel was 10 % faster, without the rows'
-// 10 %, with codes read in pieces of 1 KB 10 %, while more loads in flight (two or four windows instead of one) changed
+// ones by the cache-line requests of a CU: 16 rows x 8192 x 16384 take 20-21 us, 72 MB at 3.4-3.7 TB/s (a copy's rate, 5.0
+// TB/s, would be 14.4 us and the launch; fp32 rows, three pieces each, take 28.5 us, and one row 24).  There, without the
+// scales' loads the kernel was 10 % faster, without the rows' 10 %, with codes read in pieces of 1 KB 10 %, while more loads in flight (two or four windows instead of one) changed
 // nothing; hence fewer and fuller requests below.
 //
 // Products run on the matrix cores, 16 rows x 16 channels x 32 codes at a time, whatever M is: one
@@ -26,14 +26,15 @@
 //
 // The eight waves of a block take a run of windows each, and their sums are added over LDS.  The channels of a
 // block go by the layer's width, so that one round of blocks fills the 256 CUs (us, one row of bf16):
-//   K = 4096, N = 4096: 16 channels 4.9, 32 6.8, 64 10.2;   N = 8192: 8.1, 7.4, 10.5;   K = 8192, N = 16384: 22.2, 17.6, 18.6
-//   and with 16 rows 26.2, 20.4, 19.8.  Fewer channels than 16 (narrow layers, K >= 2048): N = 1000, K = 4096, 16 rows, 16
-//   channels 5.8, 4 channels 5.3; fp32, one rotated row 8.3 and 7.4.
+//   K = 4096, N = 4096: 16 channels 5.1, 32 6.9, 64 10.6;   N = 8192: 8.4, 7.5, 10.9;   K = 8192, N = 16384: 21.3, 17.8, 19.1
+//   and with 16 rows 25.2, 20.8, 20.7.  Fewer channels than 16 (narrow layers, K >= 2048): N = 1000, K = 4096, 16 rows, 16
+//   channels 5.3, 4 channels 4.9; fp32, one rotated row 6.4 and 5.6.
 // Rows beyond 16 count as blocks in that; where 16 to a block would take several rounds, bf16 rows go 32 to a block, which
-// then unpacks each code for both halves: 32 rows x 4096 x 16384 in 22.8 and 15.8 us, 4096 x 4000 in 9.8 and 8.3.
+// then unpacks each code for both halves: 32 rows x 4096 x 16384 in 22.8 and 16.0 us, 4096 x 4000 in 8.3 and 7.7.
 // Rows are rotated by every block for itself, or by a kernel before.  Where blocks take turns on a CU, each rotates the rows
 // again, so the rule goes by rounds of blocks as well (us, rotated in the block and before, bf16 rows):
-//   K = 1024, 1 and 12 rows    N = 1024 4.6, 5.8 and 6.3, 6.4    16384 (one round) 7.1, 8.5 and 9.3, 9.9    32768 15.5, 14.9 and 18.3, 16.2
+//   K = 1024, 1 and 12 rows    N = 1024 4.6, 5.8 and 6.3, 6.4    N = 16384 (one round) 7.1, 8.5 and 9.3, 9.9
+//                              N = 32768 15.5, 14.9 and 18.3, 16.2
 //   K = 4096, N = 1024         1 row 5.8, 9.1    5 rows 9.4, 9.7
 //             N = 32768        1 row 27.9, 30.7    3 rows 30.8, 31.6    4 rows 32.2, 31.7
 //             N = 65536        1 row 56.4, 60.1    2 rows 59.4, 60.6    3 rows 62.1, 61.0
@@ -622,8 +623,8 @@ hipError_t by_tiles(const Args<X>& a, hipStream_t st) {
     }
   }
   // Two blocks of 32 channels share a CU where their registers (bf16 rows) and LDS (rotated rows) allow it; with more than
-  // a few rows, reading the rows twice costs more than that gives: K = 4096, N = 16384, rows read and 1, 8, 16 of them 10.6, 11.4,
-  // 12.8 us (64 channels: 11.6, 12.0, 12.9), rotated and 1, 2, 3 of them 13.4, 14.5, 20.6 us (64 channels, 3: 16.5).
+  // a few rows, reading the rows twice costs more than that gives: K = 4096, N = 16384, rows read and 1, 8, 16 of them 10.6, 11.5,
+  // 12.9 us (64 channels: 11.8, 12.2, 12.9), rotated and 1, 2, 3 of them 13.3, 14.4, 20.5 us (15.1, 15.7, 16.5).
   const bool two = sizeof(X) == 2 && a.M <= (SRC == kStaged ? 8 : (SRC == kRot1024 ? 3 : 2));
   if (!fits(kRows, 32, two ? 2 : 1)) return launch_kernel<X, NP, 1, 4, 1, SRC>(a, st);
   if (!fits(kRows, 16)) return launch_kernel<X, NP, 1, 2, 1, SRC>(a, st);

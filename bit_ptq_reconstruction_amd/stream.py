@@ -21,9 +21,10 @@ class StreamBlock:
 
     The cache for ``sequences`` sequences of up to ``capacity`` tokens (rounded up to whole pages), the workspaces and the
     linears' and the attention's outputs are allocated here, so a step can be captured in a graph.  The norms and residual
-    sums are torch's and allocate theirs (under capture from the graph's pool), and so does take_frame().  ``positions`` places along each of ``axes`` axes have an angle;
-    the output of a token at another one, and of those that come after it in its sequence, is NaN.
-    A frame has up to ``frame_tokens`` tokens."""
+    sums are torch's and allocate theirs (under capture from the graph's pool), and so does take_frame().
+
+    ``positions`` places along each of ``axes`` axes have an angle; the output of a token at another one, and of those that
+    come after it in its sequence, is NaN.  A frame has up to ``frame_tokens`` tokens."""
 
     def __init__(self, qv, weights, sequences: int, capacity: int, device, heads: int = 16, axes: int = 1,
                  positions: int = 4096, base: float = 10000.0, int8_cache: bool = False, page_size: int = 64,
