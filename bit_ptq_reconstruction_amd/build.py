@@ -70,7 +70,7 @@ def build_library(verbose: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     try:
         import torch  # noqa: F401
-    except ImportError as e:
+    except (ImportError, OSError) as e:  # missing, or without a library that it loads
         torch = None
         print(f"{e}: _decode.so is not built", file=sys.stderr)
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
