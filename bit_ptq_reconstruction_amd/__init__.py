@@ -22,18 +22,27 @@ __all__ = [
     "QV_NOALLOC_SCRATCH_BYTES", "qv_w4a4_gemm_requant", "qv_w4a4_gemm_requant_workspace_size",
     # single-token entry points (decode.py)
     "qv_w4a16_gemv", "qv_w4a16_linear", "qv_w4a16_linear_workspace_size", "QVKVCache", "qv_kv_append",
-    "qv_paged_attention", "qv_paged_attention_workspace_size", "QV_KV_BF16", "QV_KV_INT8",
+    "qv_paged_attention", "qv_paged_attention_workspace_size", "QV_KV_BF16", "QV_KV_INT8", "QV_KV_FP8",
+    # entry points for runs of tokens (runs.py)
+    "qv_page_tables", "qv_run_attention", "qv_run_attention_workspace_size", "QV_RUN_OK", "QV_RUN_NO_ROOM",
+    "QV_RUN_NO_PAGES", "QV_RUN_NO_ROWS",
 ]
 
-_DECODE = frozenset(__all__[__all__.index("qv_w4a16_gemv"):])
+_RUNS = frozenset(__all__[__all__.index("qv_page_tables"):])
+_DECODE = frozenset(__all__[__all__.index("qv_w4a16_gemv"):]) - _RUNS
 
 
 def __getattr__(name: str):
-    """The single-token entry points."""
+    """The single-token entry points and those for runs of tokens."""
     if name in _DECODE:
         from . import decode
 
         globals().update({n: getattr(decode, n) for n in _DECODE})
+        return globals()[name]
+    if name in _RUNS:
+        from . import runs
+
+        globals().update({n: getattr(runs, n) for n in _RUNS})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

@@ -1,6 +1,6 @@
 // decode_binding.cpp -- the Python module _decode behind the package's single-token entry points
-// (decode.py): checks every tensor against the sizes a call implies, takes its address, and calls the C ABI
-// of include/qv_decode.h on the current stream.
+// (decode.py) and those for runs of tokens (runs.py): checks every tensor against the sizes a call implies, takes its address, and calls the C ABI
+// of include/qv_decode.h and include/qv_runs.h on the current stream.
 //
 // The calls below take a few microseconds on the device, and the same checks written in Python and
 // passed on by ctypes took 9 to 15, so a serving loop would wait for its own binding.  Host code only.
@@ -18,6 +18,7 @@
 
 #include "qv_decode.h"
 #include "qv_decode_internal.h"
+#include "qv_runs.h"
 
 namespace {
 
@@ -47,6 +48,7 @@ const char* type_name(at::ScalarType t) {
     case at::kLong: return "int64";
     case at::kHalf: return "float16";
     case at::kDouble: return "float64";
+    case at::kFloat8_e4m3fn: return "float8_e4m3fn";
     default: return c10::toString(t);
   }
 }
@@ -283,9 +285,9 @@ struct Cache {
 PyObject* kv_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("QVKVCache", n, 4, [&](Call& c) -> PyObject* {
     const at::Tensor &k = c.tensor("k_pages", a[0]), &v = c.tensor("v_pages", a[1]);
-    const bool q8 = k.scalar_type() == at::kChar;
+    const bool fp8 = k.scalar_type() == at::kFloat8_e4m3fn, q8 = fp8 || k.scalar_type() == at::kChar;
     if ((!q8 && k.scalar_type() != at::kBFloat16) || k.dim() != 4)
-      c.bad("k_pages", k, "bfloat16 or int8 [pages, heads, page_size, D]");
+      c.bad("k_pages", k, "bfloat16, int8 or float8_e4m3fn [pages, heads, page_size, D]");
     if (v.scalar_type() != k.scalar_type() || !v.sizes().equals(k.sizes()) || !v.strides().equals(k.strides()))
       c.bad("v_pages", v, "type, shape and strides of k_pages");
     const int64_t D = k.size(3);
@@ -301,7 +303,14 @@ PyObject* kv_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
       for (int i = 0; i < 2; ++i) {
         const char* name = i ? "v_scale" : "k_scale";
         s[i] = &c.tensor(name, a[2 + i]);
-        c.dense(name, *s[i], at::kFloat, {k.size(0), k.size(1), k.size(2)});
+        int64_t scales = k.size(2);  // of a page and head
+        if (fp8) {
+          scales = s[i]->dim() == 3 ? s[0]->size(2) : 0;
+          if (scales <= 0 || k.size(2) % scales != 0 || k.size(2) / scales % 16 != 0)
+            c.bad(name, *s[i], "[pages, heads, blocks] with blocks of a multiple of 16 tokens that divides the page size " +
+                                   std::to_string(k.size(2)));
+        }
+        c.dense(name, *s[i], at::kFloat, {k.size(0), k.size(1), scales});
       }
     } else if (a[2] != Py_None || a[3] != Py_None) {
       c.bad("a bfloat16 cache has no scales");
@@ -322,7 +331,8 @@ PyObject* kv_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     out.c.page_stride = stride[0];
     out.c.head_stride = stride[1];
     out.c.token_stride = stride[2];
-    out.c.dtype = q8 ? QV_KV_INT8 : QV_KV_BF16;
+    out.c.dtype = fp8 ? QV_KV_FP8 : (q8 ? QV_KV_INT8 : QV_KV_BF16);
+    out.c.scale_tokens = fp8 ? (int32_t)(k.size(2) / s[0]->size(2)) : 0;
     out.device = c.device;
     return Py_BuildValue("y#LLLL", (const char*)&out, (Py_ssize_t)sizeof out, (long long)k.size(0),
                          (long long)k.size(1), (long long)k.size(2), (long long)D);
@@ -424,12 +434,79 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Q, starts, max_run, cache, page_table, lens, O, workspace, scale, window, sinks, causal, stream
+PyObject* run_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("qv_run_attention", n, 13, [&](Call& c) {
+    const Cache& kv = cache_of(c, a[3]);
+    c.on_device(kv.device);
+    const at::Tensor &Q = c.tensor("Q", a[0]), &table = c.tensor("page_table", a[4]), &lens = c.tensor("lens", a[5]),
+                     &O = c.tensor("O", a[6]), &work = c.tensor("workspace", a[7]);
+    const int64_t D = kv.c.head_dim;
+    if (kv.c.heads <= 0) c.bad("the cache has no heads");
+    if (Q.dim() != 3 || Q.size(1) == 0 || Q.size(1) % kv.c.heads != 0 || Q.size(2) != D)
+      c.bad("Q", Q, "[T, a multiple of " + std::to_string(kv.c.heads) + " heads, " + std::to_string(D) + "]");
+    const int64_t T = Q.size(0), Hq = Q.size(1), max_run = whole(a[2]);
+    const qv_dtype type = c.float_type("Q", Q);
+    const qv_heads q = c.heads("Q", Q, T, Hq, D, type), o = c.output("O", O, T, Hq, D, type);
+    const int64_t ld = c.table(table), B = table.size(0);
+    c.dense("lens", lens, at::kInt, {B});
+    const at::Tensor* starts = a[1] == Py_None ? nullptr : &c.tensor("starts", a[1]);
+    if (starts) c.dense("starts", *starts, at::kInt, {B + 1});
+    if (max_run < 0 || max_run > T) c.bad("max_run " + std::to_string(max_run) + " of " + std::to_string(T) + " rows");
+    if (!starts && (T != B || max_run > 1))
+      c.bad(std::to_string(T) + " rows of " + std::to_string(B) + " sequences in runs of up to " + std::to_string(max_run) +
+            " need starts");
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AsDouble(a[8]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+    const int64_t window = whole(a[9]), sinks = whole(a[10]);
+    if (window < 0) c.bad("window " + std::to_string(window) + " must not be negative");
+    if (sinks < 0) c.bad("sinks " + std::to_string(sinks) + " must not be negative");
+    const int causal = PyObject_IsTrue(a[11]);
+    if (causal < 0) throw Raised{};
+    void* w = c.workspace(
+        work, qv_run_attention_workspace_size(T, B, max_run, Hq, kv.c.heads, D, table.size(1) * kv.c.page_size));
+    for (const at::Tensor* t : {&Q, starts, &table, &lens, &O, &work})
+      if (t) c.on_gpu(*t);
+    const c10::hip::HIPGuard on((c10::DeviceIndex)c.device);
+    return done(c, qv_run_attention(&q, type, T, Hq, (const int32_t*)address(starts), B, max_run, &kv.c,
+                                    (const int32_t*)table.data_ptr(), table.size(1), ld, (const int32_t*)lens.data_ptr(),
+                                    (float)scale, window, sinks, causal, &o, w, (size_t)work.numel(), c.stream(a[12])));
+  });
+}
+
+// runs, lens, free_pages, free_count, page_size, page_table, starts, lens_out, free_left, token_seq, token_index, slots,
+// status, stream
+PyObject* page_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("qv_page_tables", n, 14, [&](Call& c) {
+    static const char* const names[] = {"runs", "lens", "free_pages", "free_count", nullptr, "page_table", "starts",
+                                        "lens_out", "free_left", "token_seq", "token_index", "slots", "status"};
+    const at::Tensor* t[13] = {};
+    for (int i = 0; i < 13; ++i)
+      if (i != 4) t[i] = &c.tensor(names[i], a[i]);
+    const int64_t page_size = whole(a[4]);
+    if (page_size <= 0) c.bad("page_size " + std::to_string(page_size) + " must be positive");
+    const int64_t ld = c.table(*t[5]), B = t[5]->size(0);
+    const int64_t F = t[2]->dim() == 1 ? t[2]->size(0) : 0, T = t[9]->dim() == 1 ? t[9]->size(0) : 0;
+    const int64_t sizes[13] = {B, B, F, 1, 0, 0, B + 1, B, 1, T, T, T, B};
+    for (int i = 0; i < 13; ++i)
+      if (i != 4 && i != 5) c.dense(names[i], *t[i], i == 11 ? at::kLong : at::kInt, {sizes[i]});
+    for (int i = 0; i < 13; ++i)
+      if (t[i]) c.on_gpu(*t[i]);
+    const c10::hip::HIPGuard on((c10::DeviceIndex)c.device);
+    auto p = [&](int i) { return (int32_t*)t[i]->data_ptr(); };
+    return done(c, qv_page_tables(p(0), p(1), B, page_size, p(2), F, p(3), p(5), t[5]->size(1), ld, p(6), p(7), p(8), p(9),
+                                  p(10), (int64_t*)t[11]->data_ptr(), T, p(12), c.stream(a[13])));
+  });
+}
+
 PyMethodDef methods[] = {
     {"w4a16_gemv", (PyCFunction)(void (*)(void))w4a16_gemv, METH_FASTCALL, nullptr},
     {"w4a16_linear", (PyCFunction)(void (*)(void))w4a16_linear, METH_FASTCALL, nullptr},
     {"kv_cache", (PyCFunction)(void (*)(void))kv_cache, METH_FASTCALL, nullptr},
     {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, nullptr},
     {"paged_attention", (PyCFunction)(void (*)(void))paged_attention, METH_FASTCALL, nullptr},
+    {"run_attention", (PyCFunction)(void (*)(void))run_attention, METH_FASTCALL, nullptr},
+    {"page_tables", (PyCFunction)(void (*)(void))page_tables, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

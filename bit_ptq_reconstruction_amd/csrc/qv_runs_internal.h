@@ -1,0 +1,40 @@
+// qv_runs_internal.h -- launchers of the kernels for runs of tokens, shared between their translation units and the C ABI
+// layer (qv_runs_abi.cpp), which validates every argument before calling one.
+#pragma once
+#include "qv_decode_internal.h"
+#include "qv_runs.h"
+
+namespace qv {
+
+struct TablesArgs {
+  const int32_t *runs, *lens;
+  int64_t B, page_size;
+  const int32_t* free_pages;
+  int64_t num_free;
+  const int32_t* free_count;
+  int32_t* page_table;
+  int64_t max_pages, ld_table;
+  int32_t *starts, *lens_out, *free_left, *token_seq, *token_index;
+  int64_t* slots;
+  int64_t T;
+  int32_t* status;
+};
+hipError_t launch_page_tables(const TablesArgs& a, hipStream_t st);
+
+struct RunArgs {
+  AttentionArgs base;  // B sequences; Q and O have T rows
+  const int32_t* starts;
+  int64_t T, max_run, sinks;
+  bool causal;
+};
+hipError_t launch_run_attention(const RunArgs& a, hipStream_t st);
+
+// Bytes of partial results that the launch may write.
+inline int64_t run_attention_bytes(int64_t T, int64_t B, int64_t max_run, int64_t q_heads, int64_t heads, int64_t head_dim,
+                                   int64_t capacity) {
+  if (max_run == 0) return 0;
+  const AttentionParts p = paged_attention_parts(B, q_heads * max_run, heads, capacity);
+  return p.split ? p.most * q_heads * max_run * (head_dim + 2) * 4 : 0;
+}
+
+}  // namespace qv

@@ -14,10 +14,10 @@ from . import QV_EPI_NONE, lib
 
 __all__ = [
     "qv_w4a16_gemv", "qv_w4a16_linear", "qv_w4a16_linear_workspace_size", "QVKVCache", "qv_kv_append",
-    "qv_paged_attention", "qv_paged_attention_workspace_size", "QV_KV_BF16", "QV_KV_INT8",
+    "qv_paged_attention", "qv_paged_attention_workspace_size", "QV_KV_BF16", "QV_KV_INT8", "QV_KV_FP8",
 ]
 
-QV_KV_BF16, QV_KV_INT8 = 0, 1
+QV_KV_BF16, QV_KV_INT8, QV_KV_FP8 = 0, 1, 2
 
 
 class QVKVCacheStruct(ctypes.Structure):
@@ -26,6 +26,11 @@ class QVKVCacheStruct(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int64),
                 ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class QVBlockCacheStruct(ctypes.Structure):
+    """qv_kv_cache with its last field, the tokens of a scale, which only FP8 caches have."""
+    _fields_ = QVKVCacheStruct._fields_ + [("scale_tokens", ctypes.c_int32)]
 
 
 class QVHeadsStruct(ctypes.Structure):
@@ -102,8 +107,9 @@ def qv_w4a16_linear(X, inv_smooth, Wq, w_scale, group: int, bias, Y, workspace, 
 
 class QVKVCache:
     """A paged cache of keys and values over the caller's tensors: k_pages, v_pages [pages, heads, page_size, D]
-    (bf16, or int8 with k_scale, v_scale [pages, heads, page_size] fp32), D 64 or 128, unit channel stride,
-    the same strides in both; a permuted [pages, page_size, heads, D] tensor fits.  Holds the tensors, checks
+    (bf16; int8 with k_scale, v_scale [pages, heads, page_size] fp32; or float8_e4m3fn with k_scale, v_scale [pages,
+    heads, blocks] fp32, one for each block of page_size / blocks tokens, a multiple of 16), D 64 or 128, unit channel
+    stride, the same strides in both; a permuted [pages, page_size, heads, D] tensor fits.  Holds the tensors, checks
     them once and allocates nothing; a tensor put in another's place needs a new QVKVCache."""
 
     __slots__ = ("_k", "_v", "_ks", "_vs", "_handle", "pages", "heads", "page_size", "head_dim")
@@ -126,7 +132,8 @@ def qv_kv_append(cache, page_table, token_seq, token_index, K, V, cos=None, sin=
     page_table [sequences, pages] int32; token_seq [T] int32 sequence of each token (None: token t is sequence t);
     token_index [T] int32 place of each token in its sequence; cos, sin [places, D / (2 axes)] fp32 (None: no
     rotation); position [T, axes] int32 with 1 or 2 axes (None: token_index).  Q [T, q_heads, D] is turned into
-    Q_out (which may be Q)."""
+    Q_out (which may be Q).  A float8_e4m3fn cache takes the tokens of a block in the order of their places, next to each
+    other; a block that was begun by an earlier call keeps its scale or has its codes rounded again by a larger one."""
     _native.kv_append(getattr(cache, "_handle", None), page_table, token_seq, token_index, K, V, cos, sin, position, Q,
                       Q_out, stream)
 

@@ -57,7 +57,7 @@ qv_status qv_w4a16_linear(const void* X, qv_dtype x_dtype, int64_t M, int64_t K,
                           qv_epilogue epi, void* Y, qv_dtype y_dtype, int64_t ldy, void* workspace,
                           size_t workspace_bytes, void* hip_stream);
 
-typedef enum { QV_KV_BF16 = 0, QV_KV_INT8 = 1 } qv_kv_dtype;
+typedef enum { QV_KV_BF16 = 0, QV_KV_INT8 = 1, QV_KV_FP8 = 2 } qv_kv_dtype;
 
 /*
  * A paged cache of keys and values: num_pages pages of page_size tokens for each of `heads` heads.
@@ -67,6 +67,11 @@ typedef enum { QV_KV_BF16 = 0, QV_KV_INT8 = 1 } qv_kv_dtype;
  *   QV_KV_BF16: bf16 values;  k_scale and v_scale are not used.
  *   QV_KV_INT8: int8 codes with one fp32 scale per token and head, k_scale / v_scale
  *               [num_pages][heads][page_size] dense; the value is code * scale, scale = max |x| / 127.
+ *   QV_KV_FP8:  8-bit floating-point codes (e4m3: 4 exponent and 3 mantissa bits, NaN, no infinities) with one fp32
+ *               scale for each block of scale_tokens tokens and head, k_scale / v_scale
+ *               [num_pages][heads][page_size / scale_tokens] dense; the value is code * scale.  qv_kv_append makes
+ *               powers of two; the attention takes any finite scale.  scale_tokens is a multiple of 16 that divides
+ *               page_size (QV_ERR_UNSUPPORTED; QV_ERR_DTYPE if it is 0).  Other caches do not use it.
  * Strides are positive multiples of 16 bytes (below 2^24 elements for token_stride, 2^31 for the others).
  */
 typedef struct {
@@ -82,6 +87,7 @@ typedef struct {
   int64_t head_stride;
   int64_t token_stride;
   int32_t dtype; /* qv_kv_dtype */
+  int32_t scale_tokens;
 } qv_kv_cache;
 
 /* Input rows [T][heads][head_dim] with unit channel stride: token t, head h at t token_stride +
@@ -116,6 +122,11 @@ typedef struct {
  * (token, head) from its rotated fp32 values: scale = max |x| / 127, code = clamp(rne(x / scale), -128,
  * 127), both quotients correctly rounded; a zero or subnormal scale becomes 0 with zero codes, and a row that
  * is not finite gets a scale of NaN with zero codes.
+ * FP8 caches: the scale of a (block, head) is the least power of two, 2^-126 or more, by which the finite new values
+ * (keys rotated, in fp32) of the block are at most 448.  A block of which a call's first token is not the first keeps its own
+ * scale if that is larger; where it is smaller, the codes of the places before are multiplied by the quotient of the
+ * scales and rounded again.  Codes are x / scale to the nearest, ties to even; a value that is not finite becomes NaN.
+ * The tokens of a block follow each other in K and V in the order of their places, without gaps.
  */
 qv_status qv_kv_append(const qv_kv_cache* cache, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
                        int64_t ld_table, const int32_t* token_seq, const int32_t* token_index, int64_t T,
