@@ -24,7 +24,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-ta
          "-packed-fp32-ops", "-Wall", "-Wno-unused-function", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["rotate_quant.hip", "w4a4_gemm.hip", "noalloc_scratch.hip", "qv_abi.cpp", "w4a16_gemv.hip", "kv_append.hip",
            "kv_append_fp8.hip", "paged_attention.hip", "qv_decode_abi.cpp", "page_tables.hip", "run_attention.hip",
-           "qv_runs_abi.cpp"]
+           "run_tiles.hip", "qv_runs_abi.cpp"]
 
 
 def _compile(src: str) -> str:

@@ -170,6 +170,13 @@ __device__ __forceinline__ float signed_byte(unsigned w) {
   return f;
 }
 
+// Two signed bytes of a dword (its low or high half) as a bf16 pair, exactly.
+template <bool HIGH>
+__device__ __forceinline__ unsigned pair_of_bytes(unsigned w) {
+  const float x = HIGH ? signed_byte<2>(w) : signed_byte<0>(w), y = HIGH ? signed_byte<3>(w) : signed_byte<1>(w);
+  return __builtin_amdgcn_perm(float_bits(y), float_bits(x), 0x07060302u);
+}
+
 // Two 8-bit floating-point codes of a dword (its low or high half) as a bf16 pair.
 template <bool HIGH>
 __device__ __forceinline__ unsigned pair_of_codes(unsigned w) {

@@ -28,11 +28,40 @@ struct RunArgs {
   bool causal;
 };
 hipError_t launch_run_attention(const RunArgs& a, hipStream_t st);
+hipError_t launch_run_tiles(const RunArgs& a, hipStream_t st);  // run_tiles.hip; with starts
+
+// Long runs go in tiles of rows, up to kRowsPerTile (query heads that share a cache head, for each token) and kTokensPerStep
+// tokens at a time.
+constexpr int64_t kRowsPerTile = 128, kTokensPerStep = 64;
+constexpr int64_t kLeastSteps = 4;     // of a part
+constexpr int64_t kTileBlocks = 512;   // that the chip holds at once
+constexpr int64_t kMostParts = 64;
+struct RunTiles {
+  int64_t items, parts;
+};
+inline RunTiles run_tiles(int64_t T, int64_t B, int64_t q_heads, int64_t heads, int64_t capacity) {
+  RunTiles t;
+  t.items = T * (q_heads / heads) / kRowsPerTile + B;
+  // One round of blocks; more than one part only where the tiles leave room for it.
+  const int64_t room = kTileBlocks / (t.items * heads), steps = capacity / (kTokensPerStep * kLeastSteps);
+  t.parts = room < steps ? room : steps;
+  if (t.parts > kMostParts) t.parts = kMostParts;
+  if (t.parts < 1) t.parts = 1;
+  return t;
+}
+
+// Whether a call goes that way.
+constexpr int64_t kFewRows = QV_RUN_FEW_ROWS;
+inline bool long_runs(int64_t max_run, int64_t q_heads, int64_t heads) { return max_run * (q_heads / heads) > kFewRows && max_run > 1; }
 
 // Bytes of partial results that the launch may write.
 inline int64_t run_attention_bytes(int64_t T, int64_t B, int64_t max_run, int64_t q_heads, int64_t heads, int64_t head_dim,
                                    int64_t capacity) {
-  if (max_run == 0) return 0;
+  if (max_run == 0 || B == 0) return 0;
+  if (long_runs(max_run, q_heads, heads)) {
+    const RunTiles t = run_tiles(T, B, q_heads, heads, capacity);
+    return t.parts > 1 ? t.parts * T * q_heads * (head_dim + 2) * 4 : 0;
+  }
   const AttentionParts p = paged_attention_parts(B, q_heads * max_run, heads, capacity);
   return p.split ? p.most * q_heads * max_run * (head_dim + 2) * 4 : 0;
 }

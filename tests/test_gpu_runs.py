@@ -406,7 +406,7 @@ def runs64(Q, starts, cache, table, lens, window, sinks, causal, scale, max_run=
 
 def rounds(max_run, share, xt):
     """Whether the probabilities of such a call are rounded to bf16."""
-    return False
+    return xt == "bf16" and max_run > 1 and max_run * share > 32
 
 
 def check(O, expect, xt, rounded, label=""):
