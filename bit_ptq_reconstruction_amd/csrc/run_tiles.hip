@@ -17,6 +17,8 @@
 // sign, as much as the result's own rounding); their sum is of the unrounded ones.  fp32 queries and their probabilities
 // are three bf16 pieces that sum to them.
 // The maximum that scales a row's probabilities is raised only when one passes 2^8 of it: sums are fp32, and the rest follows.
+#include <type_traits>
+
 #include "paged_attention.h"
 #include "qv_runs_internal.h"
 
@@ -66,6 +68,7 @@ __device__ __forceinline__ Item item_of(const Args& a, int64_t number) {
 // What the rows of a tile see: [0, sinks) and [low, high), in steps of 64 tokens without those between.
 struct Steps {
   int len, low, high, sinks, near, skip, count;  // count: steps
+  int all_low, all_high;                         // [all_low, all_high) is what every row sees
   int per, parts;                                // steps of a part; parts that have any
   __device__ __forceinline__ int first_token(int step) const { return (step < near ? step : step + skip) * kN; }
 };
@@ -78,6 +81,8 @@ __device__ __forceinline__ Steps steps_of(const TileArgs& t, const Item& i) {
   const int64_t from = (int64_t)s.len - i.run.n + first / (int)a.share, to = (int64_t)s.len - i.run.n + last / (int)a.share;
   s.high = !a.causal ? s.len : (to + 1 < 0 ? 0 : (int)(to + 1));
   s.low = a.window > 0 && from >= a.window ? (int)(from - a.window + 1) : 0;
+  s.all_high = !a.causal ? s.len : (from + 1 < 0 ? 0 : (int)(from + 1));
+  s.all_low = a.window > 0 && to >= a.window ? (int)(to - a.window + 1) : 0;
   s.sinks = a.sinks < s.high ? a.sinks : s.high;
   s.near = (s.sinks + kN - 1) / kN;
   s.skip = s.low / kN > s.near ? s.low / kN - s.near : 0;
@@ -112,6 +117,19 @@ __device__ __forceinline__ unsigned even_pair(unsigned w) {  // zeros in their p
   return (w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFFu : w;
 }
 
+// 16 bytes of each lane's address to LDS, side by side from `to` on (the same in a wave).  The compiler does not count these loads:
+// what reads them comes behind arrive().  (Its own builtin for them makes the next read of LDS wait, whatever it reads.)
+__device__ __forceinline__ void load_to_lds(const char* from, u32x4* to) {
+  const unsigned at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(at)), "v"(from)
+               : "memory", "m0");
+}
+// All loads to LDS of the block have landed, and all waves are here.
+__device__ __forceinline__ void arrive() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
 template <int D, typename X, int KIND>
 __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void tiles_kernel(TileArgs t) {
   const Args& a = t.a;
@@ -122,9 +140,8 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   constexpr int kTokens = kThreads / kPieces;     // tokens of one load of the block
   constexpr int kK = D / 16, kC = D / 32;
   constexpr int kRowPieces = D / 8;               // 16-byte pieces of a token in LDS
-  __shared__ u32x4 ks[2][kN * kRowPieces], vs[2][kN * kRowPieces];
+  __shared__ __attribute__((aligned(1024))) u32x4 ks[2][kN * kRowPieces], vs[2][kN * kRowPieces];
   __shared__ float k_scale[2][kN], v_scale[2][kN];
-  __shared__ unsigned odd[3][2];                  // tokens of a step with a value that is not finite
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, half = lane >> 5;
@@ -207,27 +224,50 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
       scale_at = (page * a.heads + h) * a.page_size + slot;
   };
 
-  // A step's keys and values on their way: this thread's pieces, and which groups of tokens have a page.
-  u32x4 kr[kPass], vr[kPass];
+  // A step's keys and values: bf16 straight into LDS, 8-bit codes by way of registers.  Where some row of the block does not see the
+  // whole step, lanes of tokens that none sees read the nearest one that is seen (or anything, if that has no page).
+  constexpr int kBuffer = kN * kRowPieces;  // pieces of a buffer
+  constexpr int kHeld = KIND == kBf16 ? 1 : kPass;
+  u32x4 kr[kHeld], vr[kHeld];
   float scale_r = 0.0f;
   const int my_token = threadIdx.x / kPieces, my_piece = threadIdx.x % kPieces;
   const uint32_t token_bytes = a.token_stride * kElem;
-  auto any_sees = [&](int tk) { return tk < steps.high && (tk >= steps.low || tk < steps.sinks); };
-  auto block_edge = [&](int t0) { return t0 < steps.low || t0 + kN > steps.high; };
-  auto load = [&](int step) {
-    if (step % 16 == first_step % 16) look_up(step);
-    const int t0 = steps.first_token(step), lane0 = 4 * ((step - first_step) % 16);
-    const bool edge = block_edge(t0);
+  const int kx_write = my_token & (kRowPieces - 1), vx_write = D == 128 ? (my_token & 3) << 2 : (my_token >> 1 & 1) << 2;
+  // The lane's piece in a token; bf16: the one whose place in LDS is the lane's.
+  const uint32_t k_piece = 16 * (KIND == kBf16 ? my_piece ^ kx_write : my_piece);
+  const uint32_t v_piece = 16 * (KIND == kBf16 ? my_piece ^ vx_write : my_piece);
+  const uint32_t k_bytes = (my_token % 16) * token_bytes + k_piece, v_bytes = (my_token % 16) * token_bytes + v_piece;
+  auto load = [&](int step) {  // returns which groups of tokens have a page
+    const int number = step - first_step, lane0 = 4 * (number % 16);
+    if (number % 16 == 0) look_up(step);
+    const int t0 = steps.first_token(step);
+    const unsigned paged = __ballot(at >= 0) >> lane0 & 15;
+    if (paged == 0) return paged;
+    const bool whole = paged == 15 && t0 >= steps.all_low && t0 + kN <= steps.all_high;
 #pragma unroll
     for (int i = 0; i < kPass; ++i) {
-      const int tk = i * kTokens + my_token;
-      const int group = (i * kTokens + wave * (kTokens / 4)) / 16;  // the same in a wave
-      const int64_t from = lane_value(at, lane0 + group);
-      kr[i] = vr[i] = u32x4{0, 0, 0, 0};
-      if (from >= 0 && (!edge || any_sees(t0 + tk))) {
-        const int64_t off = from * kElem + (uint64_t)(tk % 16) * token_bytes + 16 * my_piece;
-        kr[i] = *reinterpret_cast<const u32x4*>(a.kp + off);
-        vr[i] = *reinterpret_cast<const u32x4*>(a.vp + off);
+      const char *k, *v;
+      if (whole) {
+        const int group = (i * kTokens + wave * (kTokens / 4)) / 16;  // the same in a wave
+        const int64_t from = lane_value(at, lane0 + group) * kElem;
+        k = a.kp + from + k_bytes;
+        v = a.vp + from + v_bytes;
+      } else {
+        int tk = t0 + i * kTokens + my_token;
+        tk = tk < steps.high ? tk : steps.high - 1;
+        if (tk < steps.low && tk >= steps.sinks) tk = steps.sinks > t0 ? steps.sinks - 1 : steps.low;
+        const int64_t group = __shfl(at, lane0 + ((tk - t0) >> 4)), from = (group < 0 ? 0 : group) * kElem + (uint64_t)(tk % 16) * token_bytes;
+        k = a.kp + from + k_piece;
+        v = a.vp + from + v_piece;
+      }
+      if constexpr (KIND == kBf16) {
+        // A wave's 64 pieces go side by side.
+        const int to = ((number & 1) * kBuffer + (i * 4 + wave) * 64);
+        load_to_lds(k, &ks[0][0] + to);
+        load_to_lds(v, &vs[0][0] + to);
+      } else {
+        kr[i] = *reinterpret_cast<const u32x4*>(k);
+        vr[i] = *reinterpret_cast<const u32x4*>(v);
       }
     }
     if constexpr (KIND != kBf16) {
@@ -236,57 +276,29 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
         scale_r = from >= 0 ? (wave == 0 ? a.ks : a.vs)[KIND == kFp8 ? s : s + lane % 16] : 0.0f;
       }
     }
-    return __ballot(at >= 0) >> lane0 & 15;  // groups of the step that have a page
+    return paged;
   };
-  auto stage = [&](int step) {
-    const int t0 = steps.first_token(step), buffer = (step - first_step) & 1, slot = (step - first_step) % 3;
-    const bool edge = block_edge(t0) || a.causal || a.window > 0;
+  auto stage = [&](int step) {  // 8-bit codes as bf16
+    const int buffer = (step - first_step) & 1;
+    u32x4* const kt = &ks[0][0] + buffer * kBuffer + my_token * kRowPieces;
+    u32x4* const vt = &vs[0][0] + buffer * kBuffer + my_token * kRowPieces;
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      const int tk = i * kTokens + my_token;
-      u32x4* const kt = &ks[buffer][tk * kRowPieces];
-      u32x4* const vt = &vs[buffer][tk * kRowPieces];
-      const int kx = tk & (kRowPieces - 1), vx = D == 128 ? (tk & 3) << 2 : (tk >> 1 & 1) << 2;
-      if constexpr (KIND == kBf16) {
-        kt[my_piece ^ kx] = kr[i];
-        vt[my_piece ^ vx] = vr[i];
-        if (edge) {
-          bool any = false;
+    for (int i = 0; i < kHeld; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) any |= odd_pair(vr[i][j]);
-          if (any) atomicOr(&odd[slot][tk >> 5], 1u << (tk & 31));
+      for (int u = 0; u < 2; ++u) {
+        u32x4 k, v;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const unsigned kw = kr[i][2 * u + j], vw = vr[i][2 * u + j];
+          k[2 * j] = KIND == kFp8 ? pair_of_codes<false>(kw) : pair_of_bytes<false>(kw);
+          k[2 * j + 1] = KIND == kFp8 ? pair_of_codes<true>(kw) : pair_of_bytes<true>(kw);
+          v[2 * j] = KIND == kFp8 ? pair_of_codes<false>(vw) : pair_of_bytes<false>(vw);
+          v[2 * j + 1] = KIND == kFp8 ? pair_of_codes<true>(vw) : pair_of_bytes<true>(vw);
         }
-      } else {
-        u32x4 k[2], v[2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const unsigned kw = kr[i][j], vw = vr[i][j];
-            if constexpr (KIND == kFp8) {
-              k[j >> 1][2 * (j & 1) + u] = u ? pair_of_codes<true>(kw) : pair_of_codes<false>(kw);
-              v[j >> 1][2 * (j & 1) + u] = u ? pair_of_codes<true>(vw) : pair_of_codes<false>(vw);
-            } else {
-              k[j >> 1][2 * (j & 1) + u] = u ? pair_of_bytes<true>(kw) : pair_of_bytes<false>(kw);
-              v[j >> 1][2 * (j & 1) + u] = u ? pair_of_bytes<true>(vw) : pair_of_bytes<false>(vw);
-            }
-          }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          kt[(2 * my_piece + u) ^ kx] = k[u];
-          vt[(2 * my_piece + u) ^ vx] = v[u];
-        }
-        if (KIND == kFp8 && edge) {
-          bool any = false;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) any |= (((vr[i][j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-          if (any) atomicOr(&odd[slot][tk >> 5], 1u << (tk & 31));
-        }
+        kt[i * kTokens * kRowPieces + ((2 * my_piece + u) ^ kx_write)] = k;
+        vt[i * kTokens * kRowPieces + ((2 * my_piece + u) ^ vx_write)] = v;
       }
-    }
-    if constexpr (KIND != kBf16) {
-      if (wave < 2) (wave == 0 ? k_scale : v_scale)[buffer][lane] = scale_r;
-    }
+    if (wave < 2) (wave == 0 ? k_scale : v_scale)[buffer][lane] = scale_r;
   };
 
   f32x16 o[kC];
@@ -294,137 +306,150 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   for (int i = 0; i < kC; ++i) o[i] = f32x16{};
   float m = kLowest, l = 0.0f;  // of the lane's row, in bits; l of its half of the tokens
 
-  if (threadIdx.x < 6) odd[threadIdx.x >> 1][threadIdx.x & 1] = 0;
-  __syncthreads();
-  uint64_t paged = 0, paged_next = 0;
-  if (first_step < last_step) {
-    paged = load(first_step);
-    stage(first_step);
-  }
-  __syncthreads();
+  // Where the lane reads operands in LDS: piece 2 k + half of token r, and four channels of token 4 half + (lane / 4) % 4.
+  const int k_row = r * kRowPieces, k_xor = r & (kRowPieces - 1);
+  const int v_token = 4 * half + (lane >> 2 & 3), v_xor = D == 128 ? (v_token & 3) << 2 : (v_token >> 1 & 1) << 2;
+  const int v_four = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
+  int k_at[kK], v_at[kC];
+#pragma unroll
+  for (int k = 0; k < kK; ++k) k_at[k] = k_row + ((2 * k + half) ^ k_xor);
+#pragma unroll
+  for (int d = 0; d < kC; ++d) v_at[d] = 2 * (v_token * kRowPieces + ((4 * d + v_four) ^ v_xor)) + (lane & 1);  // in 8 bytes
 
-  for (int step = first_step; step < last_step; ++step) {
-    const int buffer = (step - first_step) & 1, t0 = steps.first_token(step);
-    const bool more = step + 1 < last_step;
-    if (more) paged_next = load(step + 1);
-    if (threadIdx.x < 2) odd[(step - first_step + 2) % 3][threadIdx.x] = 0;  // read a step ago, used in the next but one
-
-    if (live && t0 < any_high && (t0 + kN > any_low || t0 < a.sinks)) {
-      const bool edge = t0 < all_low || t0 + kN > all_high || paged != 15;
-      float s[2][16];
-      float top = -INFINITY;
+  // One step.  `edge`: some row of the wave may not see all of it.  CAREFUL: values that are not finite, which would reach the rows
+  // that do not see their token through their zero probabilities, are left out of the product and added to the rows that see them.
+  auto work = [&](auto careful, bool edge, int step, int t0, unsigned paged) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+    const int buffer = (step - first_step) & 1;
+    float s[2][16];
+    float top = -INFINITY;
+    const u32x4* const kt = &ks[0][0] + buffer * kBuffer;
+    f32x16 acc[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+    for (int k = 0; k < kK; ++k)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        f32x16 acc = f32x16{};
-        const u32x4* const kt = &ks[buffer][(32 * u + r) * kRowPieces];
-        const int kx = r & (kRowPieces - 1);
+        const bf16x8 f = __builtin_bit_cast(bf16x8, kt[k_at[k] + 32 * u * kRowPieces]);
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-          const bf16x8 f = __builtin_bit_cast(bf16x8, kt[(2 * k + half) ^ kx]);
-#pragma unroll
-          for (int n = NP - 1; n >= 0; --n) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k][n], acc, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[u][i] = acc[i];
-        if constexpr (KIND != kBf16) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 f = *reinterpret_cast<const f32x4*>(&k_scale[buffer][32 * u + 8 * g + 4 * half]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[u][4 * g + i] *= f[i];
-          }
-        }
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int tk = 32 * u + 8 * (i >> 2) + 4 * half + (i & 3);
-            s[u][i] = sees(t0 + tk) && (paged >> (tk >> 4) & 1) ? s[u][i] : -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        for (int n = NP - 1; n >= 0; --n) acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k][n], acc[u], 0, 0, 0);
       }
-      top = fmaxf(top, __shfl_xor(top, 32)) * c;
-      if (__any(top > m + kSlack)) {
-        top = fmaxf(top, m);
-        const float shrink = exp2_raw(m - top);
-        m = top;
-        l *= shrink;
 #pragma unroll
-        for (int i = 0; i < kC; ++i)
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[i][j] *= shrink;
+      for (int i = 0; i < 16; ++i) s[u][i] = acc[u][i];
+      if constexpr (KIND != kBf16) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(&k_scale[buffer][32 * u + 8 * g + 4 * half]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][4 * g + i] *= f[i];
+        }
       }
+    }
+    if (edge) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[u][i] = exp2_raw(fmaf(s[u][i], c, -m));
-          l += s[u][i];
+          const int tk = t0 + 32 * u + 8 * (i >> 2) + 4 * half + (i & 3);
+          const bool seen = (tk < high) & ((tk >= low) | (tk < a.sinks)) & ((paged >> (2 * u + (i >> 3)) & 1) != 0);
+          s[u][i] = seen ? s[u][i] : -INFINITY;
         }
-      if constexpr (KIND != kBf16) {
+    }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 f = *reinterpret_cast<const f32x4*>(&v_scale[buffer][32 * u + 8 * g + 4 * half]);
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+    top = fmaxf(top, __shfl_xor(top, 32)) * c;
+    if (__any(top > m + kSlack)) {
+      top = fmaxf(top, m);
+      const float shrink = exp2_raw(m - top);
+      m = top;
+      l *= shrink;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float& p = s[u][4 * g + i];
-              const int tk = 32 * u + 8 * g + 4 * half + i;
-              p = !edge || (sees(t0 + tk) && (paged >> (tk >> 4) & 1)) ? p * f[i] : 0.0f;  // a scale that a row does not see may be anything
-            }
-          }
+      for (int i = 0; i < kC; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= shrink;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[u][i] = exp2_raw(fmaf(s[u][i], c, -m));
+        l += s[u][i];
       }
-      const uint64_t odd_tokens = edge && KIND != kInt8 ? (uint64_t)odd[(step - first_step) % 3][1] << 32 | odd[(step - first_step) % 3][0] : 0;
+    if constexpr (KIND != kBf16) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          bf16x8 p[NP];
-          if constexpr (NP == 1) {
-            u32x4 w;
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(&v_scale[buffer][32 * u + 8 * g + 4 * half]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack(s[u][8 * g + 2 * i], s[u][8 * g + 2 * i + 1]);
-            p[0] = __builtin_bit_cast(bf16x8, w);
-          } else {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = s[u][8 * g + i];
-#pragma unroll
-            for (int n = 0; n < NP; ++n) {
-              u32x4 w;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = cut(x[2 * i], x[2 * i + 1]);
-              p[n] = __builtin_bit_cast(bf16x8, w);
-            }
-          }
-#pragma unroll
-          for (int d = 0; d < kC; ++d) {
-            u32x4 w;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int tk = 32 * u + 16 * g + 8 * z + 4 * half + (lane >> 2 & 3);
-              const int piece = 4 * d + 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
-              const int vx = D == 128 ? (tk & 3) << 2 : (tk >> 1 & 1) << 2;
-              s16x4* const from = reinterpret_cast<s16x4*>(&vs[buffer][tk * kRowPieces + (piece ^ vx)]) + (lane & 1);
-              const u32x2 x = __builtin_bit_cast(
-                  u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)from));
-              w[2 * z] = x[0];
-              w[2 * z + 1] = x[1];
-            }
-            if (odd_tokens) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = even_pair(w[i]);
-            }
-            const bf16x8 f = __builtin_bit_cast(bf16x8, w);
-#pragma unroll
-            for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p[n], o[d], 0, 0, 0);
+          for (int i = 0; i < 4; ++i) {
+            float& p = s[u][4 * g + i];
+            const int tk = 32 * u + 8 * g + 4 * half + i;
+            // A scale of a token that the row does not see may be anything.
+            p = !CAREFUL || (sees(t0 + tk) & ((paged >> (2 * u + (g >> 1)) & 1) != 0)) ? p * f[i] : 0.0f;
           }
         }
-      // Values that are not finite would reach the rows that do not see their token through their zero probabilities: they
-      // were left out above and are added to the rows that see them.
-      for (uint64_t left = odd_tokens; left; left &= left - 1) {
+    }
+    s16x4* const vt = reinterpret_cast<s16x4*>(&vs[0][0] + buffer * kBuffer);
+    auto values = [&](int u, int g, int d) {  // operand of 16 tokens and 32 channels
+      u32x4 w;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        s16x4* const from = vt + v_at[d] + 2 * (32 * u + 16 * g + 8 * z) * kRowPieces;
+        const u32x2 x = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)from));
+        w[2 * z] = x[0];
+        w[2 * z + 1] = x[1];
+      }
+      return w;
+    };
+    auto probabilities = [&](int u, int g, bf16x8 (&p)[NP]) {
+      if constexpr (NP == 1) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack(s[u][8 * g + 2 * i], s[u][8 * g + 2 * i + 1]);
+        p[0] = __builtin_bit_cast(bf16x8, w);
+      } else {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = s[u][8 * g + i];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+          u32x4 w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = cut(x[2 * i], x[2 * i + 1]);
+          p[n] = __builtin_bit_cast(bf16x8, w);
+        }
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        bf16x8 p[NP];
+        probabilities(u, g, p);
+#pragma unroll
+        for (int d = 0; d < kC; ++d) {
+          u32x4 w = values(u, g, d);
+          if constexpr (CAREFUL) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = even_pair(w[i]);
+          }
+          const bf16x8 f = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+          for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p[n], o[d], 0, 0, 0);
+        }
+      }
+    if constexpr (CAREFUL) {
+      const u32x4* const mine = &vs[buffer][lane * kRowPieces];  // lane i looks at token i
+      bool any = false;
+      for (int j = 0; j < kRowPieces; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= odd_pair(mine[j][i]);
+      for (uint64_t left = __ballot(any); left; left &= left - 1) {
         const int tk = __builtin_ctzll(left);
         float p = 0.0f;
 #pragma unroll
@@ -445,9 +470,41 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
           }
       }
     }
-    if (more) stage(step + 1);
-    paged = paged_next;
-    __syncthreads();
+  };
+
+  auto pass = [&](auto careful) {
+    unsigned paged = 0, paged_next = 0;
+    if (first_step < last_step) {
+      paged = load(first_step);
+      if constexpr (KIND != kBf16) stage(first_step);
+    }
+    arrive();
+    for (int step = first_step; step < last_step; ++step) {
+      const int t0 = steps.first_token(step);
+      const bool more = step + 1 < last_step;
+      if (more) paged_next = load(step + 1);
+      if (live && paged != 0 && t0 < any_high && (t0 + kN > any_low || t0 < a.sinks))
+        work(careful, t0 < all_low || t0 + kN > all_high || paged != 15, step, t0, paged);
+      if constexpr (KIND != kBf16) {
+        if (more) stage(step + 1);
+      }
+      paged = paged_next;
+      arrive();
+    }
+  };
+  pass(std::false_type{});
+  // Again, with care, where something was not finite.
+  float zero = 0.0f * l;
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) zero = fmaf(o[i][j], 0.0f, zero);
+  if (__syncthreads_or(live && zero != 0.0f)) {  // NaN
+    m = kLowest;
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) o[i] = f32x16{};
+    pass(std::true_type{});
   }
 
   l += __shfl_xor(l, 32);
