@@ -33,20 +33,27 @@ hipError_t launch_run_tiles(const RunArgs& a, hipStream_t st);  // run_tiles.hip
 // Long runs go in tiles of rows, up to kRowsPerTile (query heads that share a cache head, for each token) and kTokensPerStep
 // tokens at a time.
 constexpr int64_t kRowsPerTile = 128, kTokensPerStep = 64;
-constexpr int64_t kLeastSteps = 4;     // of a part
-constexpr int64_t kTileBlocks = 512;   // that the chip holds at once
+constexpr int64_t kLeastSteps = 4;   // of a part
 constexpr int64_t kMostParts = 64;
+constexpr int64_t kTileCUs = 256;
 struct RunTiles {
   int64_t items, parts;
 };
-inline RunTiles run_tiles(int64_t T, int64_t B, int64_t q_heads, int64_t heads, int64_t capacity) {
+// Tiles of rows, and into how many parts the tokens that one sees are cut.  A CU works on its blocks side by side and is well used
+// with two or more, so a call takes about (blocks of the CU that has most) x (steps of a block and its start), half as much again where
+// that is one block; each part costs the join as much as a step.  `seen`: tokens that a tile's rows see, at most; `room`: parts
+// that the workspace holds.
+inline RunTiles run_tiles(int64_t T, int64_t B, int64_t q_heads, int64_t heads, int64_t seen, int64_t room = kMostParts) {
   RunTiles t;
   t.items = T * (q_heads / heads) / kRowsPerTile + B;
-  // One round of blocks; more than one part only where the tiles leave room for it.
-  const int64_t room = kTileBlocks / (t.items * heads), steps = capacity / (kTokensPerStep * kLeastSteps);
-  t.parts = room < steps ? room : steps;
-  if (t.parts > kMostParts) t.parts = kMostParts;
-  if (t.parts < 1) t.parts = 1;
+  t.parts = 1;
+  const int64_t steps = seen / kTokensPerStep + 1, blocks = t.items * heads, most = steps / kLeastSteps;
+  int64_t best = 0;
+  for (int64_t p = 1; p <= room && p <= most && (p == 1 || blocks * (p - 1) < 8 * kTileCUs); ++p) {
+    const int64_t on_a_cu = (blocks * p + kTileCUs - 1) / kTileCUs, each = (steps + p - 1) / p + 6;
+    const int64_t cost = 2 * on_a_cu * each + (on_a_cu == 1 ? each : 0) + (p > 1 ? 2 * p + 12 : 0);
+    if (p == 1 || cost < best) best = cost, t.parts = p;
+  }
   return t;
 }
 

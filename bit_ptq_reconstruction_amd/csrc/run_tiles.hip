@@ -28,6 +28,7 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = (int)kRowsPerTile, kN = (int)kTokensPerStep;  // of a block; tokens at a time
@@ -117,13 +118,28 @@ __device__ __forceinline__ unsigned even_pair(unsigned w) {  // zeros in their p
   return (w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFFu : w;
 }
 
-// 16 bytes of each lane's address to LDS, side by side from `to` on (the same in a wave).  The compiler does not count these loads:
-// what reads them comes behind arrive().  (Its own builtin for them makes the next read of LDS wait, whatever it reads.)
-__device__ __forceinline__ void load_to_lds(const char* from, u32x4* to) {
-  const unsigned at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)to;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(at)), "v"(from)
-               : "memory", "m0");
+// What the numbers of a token's 16-byte pieces are changed by in LDS: pieces of one number of 16 neighbouring keys, and pieces
+// 4 i to 4 i + 3 of four neighbouring values, lie on different banks.
+template <int D>
+__device__ __forceinline__ int key_xor(int token) {
+  return D == 128 ? token & 15 : token >> 1 & 7;
 }
+template <int D>
+__device__ __forceinline__ int value_xor(int token) {
+  return D == 128 ? (token & 3) << 2 : (token >> 1 & 1) << 2;
+}
+
+// 16 bytes of each lane's address to LDS, side by side from byte `to` on.  The compiler does not count these loads: what reads
+// them comes behind arrive().  (Its own builtin for them makes the next read of LDS wait, whatever it reads.)
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t lane_bytes, uint32_t to) {  // base and `to` the same in a wave
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(lane_bytes), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+}
+// Loads above stay in their branch.  (Merged with those of another branch, the compiler gave them an address that one way there
+// left undefined.)
+__device__ __forceinline__ void keep_apart() { asm volatile("" ::: "memory"); }
 // All loads to LDS of the block have landed, and all waves are here.
 __device__ __forceinline__ void arrive() {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -204,7 +220,7 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   }
   const float c = scale > 0.0f ? scale : 1.0f;
 
-  // Lane i knows where group i of 16 tokens of the next 16 steps begins: an offset from the cache's start, -1 without a page.
+  // Lane i knows where group i of 16 tokens of the next 16 steps begins: bytes from the cache's start, -1 without a page.
   const int32_t* const table = a.table + (int64_t)item.b * a.ld_table;
   int64_t at = -1;
   int64_t scale_at = 0;
@@ -217,7 +233,7 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
     if ((int)from >= steps.high) return;
     const int64_t page = table[entry];
     if (page < 0 || page >= a.num_pages) return;
-    at = page * a.page_stride + h * a.head_stride + (int64_t)slot * a.token_stride;
+    at = (page * a.page_stride + h * a.head_stride + (int64_t)slot * a.token_stride) * kElem;
     if constexpr (KIND == kFp8)
       scale_at = (page * a.heads + h) * (a.page_size / a.scale_tokens) + slot / a.scale_tokens;
     else
@@ -232,43 +248,55 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   float scale_r = 0.0f;
   const int my_token = threadIdx.x / kPieces, my_piece = threadIdx.x % kPieces;
   const uint32_t token_bytes = a.token_stride * kElem;
-  const int kx_write = my_token & (kRowPieces - 1), vx_write = D == 128 ? (my_token & 3) << 2 : (my_token >> 1 & 1) << 2;
+  const int kx_write = key_xor<D>(my_token), vx_write = value_xor<D>(my_token);
   // The lane's piece in a token; bf16: the one whose place in LDS is the lane's.
   const uint32_t k_piece = 16 * (KIND == kBf16 ? my_piece ^ kx_write : my_piece);
   const uint32_t v_piece = 16 * (KIND == kBf16 ? my_piece ^ vx_write : my_piece);
   const uint32_t k_bytes = (my_token % 16) * token_bytes + k_piece, v_bytes = (my_token % 16) * token_bytes + v_piece;
+  // Where a wave's pieces of the first buffer go, and the values behind the keys.
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&ks[0][0] + 1024 * wave);
+  const uint32_t values_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&vs[0][0] + 1024 * wave) - lds0;
   auto load = [&](int step) {  // returns which groups of tokens have a page
     const int number = step - first_step, lane0 = 4 * (number % 16);
     if (number % 16 == 0) look_up(step);
     const int t0 = steps.first_token(step);
     const unsigned paged = __ballot(at >= 0) >> lane0 & 15;
-    if (paged == 0) return paged;
+    if (paged == 0) {
+      keep_apart();
+      return paged;
+    }
     const bool whole = paged == 15 && t0 >= steps.all_low && t0 + kN <= steps.all_high;
+    const uint32_t to = lds0 + (number & 1) * (16 * kBuffer);
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      const char *k, *v;
-      if (whole) {
-        const int group = (i * kTokens + wave * (kTokens / 4)) / 16;  // the same in a wave
-        const int64_t from = lane_value(at, lane0 + group) * kElem;
-        k = a.kp + from + k_bytes;
-        v = a.vp + from + v_bytes;
-      } else {
+      for (int i = 0; i < kPass; ++i) {
+        const int64_t from = lane_value(at, lane0 + (i * kTokens + wave * (kTokens / 4)) / 16);  // a group is the same in a wave
+        if constexpr (KIND == kBf16) {  // a wave's 64 pieces go side by side
+          load_to_lds(a.kp + from, k_bytes, to + i * 4096);
+          load_to_lds(a.vp + from, v_bytes, to + i * 4096 + values_at);
+        } else {
+          kr[i] = *reinterpret_cast<const u32x4*>(a.kp + from + k_bytes);
+          vr[i] = *reinterpret_cast<const u32x4*>(a.vp + from + v_bytes);
+        }
+      }
+      keep_apart();
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPass; ++i) {
         int tk = t0 + i * kTokens + my_token;
         tk = tk < steps.high ? tk : steps.high - 1;
         if (tk < steps.low && tk >= steps.sinks) tk = steps.sinks > t0 ? steps.sinks - 1 : steps.low;
-        const int64_t group = __shfl(at, lane0 + ((tk - t0) >> 4)), from = (group < 0 ? 0 : group) * kElem + (uint64_t)(tk % 16) * token_bytes;
-        k = a.kp + from + k_piece;
-        v = a.vp + from + v_piece;
+        const int64_t group = __shfl(at, lane0 + ((tk - t0) >> 4));
+        const int64_t from = (group < 0 ? 0 : group) + (uint64_t)(tk & 15) * token_bytes;
+        if constexpr (KIND == kBf16) {
+          load_to_lds(a.kp + from + k_piece, to + i * 4096);
+          load_to_lds(a.vp + from + v_piece, to + i * 4096 + values_at);
+        } else {
+          kr[i] = *reinterpret_cast<const u32x4*>(a.kp + from + k_piece);
+          vr[i] = *reinterpret_cast<const u32x4*>(a.vp + from + v_piece);
+        }
       }
-      if constexpr (KIND == kBf16) {
-        // A wave's 64 pieces go side by side.
-        const int to = ((number & 1) * kBuffer + (i * 4 + wave) * 64);
-        load_to_lds(k, &ks[0][0] + to);
-        load_to_lds(v, &vs[0][0] + to);
-      } else {
-        kr[i] = *reinterpret_cast<const u32x4*>(k);
-        vr[i] = *reinterpret_cast<const u32x4*>(v);
-      }
+      keep_apart();
     }
     if constexpr (KIND != kBf16) {
       if (wave < 2) {  // 64 scales of keys, 64 of values
@@ -307,8 +335,8 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   float m = kLowest, l = 0.0f;  // of the lane's row, in bits; l of its half of the tokens
 
   // Where the lane reads operands in LDS: piece 2 k + half of token r, and four channels of token 4 half + (lane / 4) % 4.
-  const int k_row = r * kRowPieces, k_xor = r & (kRowPieces - 1);
-  const int v_token = 4 * half + (lane >> 2 & 3), v_xor = D == 128 ? (v_token & 3) << 2 : (v_token >> 1 & 1) << 2;
+  const int k_row = r * kRowPieces, k_xor = key_xor<D>(r);
+  const int v_token = 4 * half + (lane >> 2 & 3), v_xor = value_xor<D>(v_token);
   const int v_four = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
   int k_at[kK], v_at[kC];
 #pragma unroll
@@ -333,6 +361,14 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n) acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k][n], acc[u], 0, 0, 0);
       }
+    if constexpr (NP == 1) {  // six reads ahead
+      __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -360,7 +396,8 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-    top = fmaxf(top, __shfl_xor(top, 32)) * c;
+    const u32x2 both = __builtin_amdgcn_permlane32_swap(float_bits(top), float_bits(top), false, false);  // the two halves' maxima
+    top = fmaxf(bits_float(both[0]), bits_float(both[1])) * c;
     if (__any(top > m + kSlack)) {
       top = fmaxf(top, m);
       const float shrink = exp2_raw(m - top);
@@ -371,28 +408,38 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] *= shrink;
     }
+    // Probabilities of 16 tokens, numbers 8 g to 8 g + 7 of half u.
+    auto probabilities = [&](int u, int g, bf16x8 (&p)[NP]) {
+      float x[8];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[u][i] = exp2_raw(fmaf(s[u][i], c, -m));
-        l += s[u][i];
+      for (int i = 0; i < 8; ++i) {
+        float& y = s[u][8 * g + i];
+        y = exp2_raw(fmaf(y, c, -m));
+        l += y;
       }
-    if constexpr (KIND != kBf16) {
+      if constexpr (KIND != kBf16) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(&v_scale[buffer][32 * u + 8 * g + 4 * half]);
+        for (int z = 0; z < 2; ++z) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(&v_scale[buffer][32 * u + 16 * g + 8 * z + 4 * half]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float& p = s[u][4 * g + i];
-            const int tk = 32 * u + 8 * g + 4 * half + i;
+            float& y = s[u][8 * g + 4 * z + i];
+            const int tk = 32 * u + 16 * g + 8 * z + 4 * half + i;
             // A scale of a token that the row does not see may be anything.
-            p = !CAREFUL || (sees(t0 + tk) & ((paged >> (2 * u + (g >> 1)) & 1) != 0)) ? p * f[i] : 0.0f;
+            y = !CAREFUL || (sees(t0 + tk) & ((paged >> (2 * u + g) & 1) != 0)) ? y * f[i] : 0.0f;
           }
         }
-    }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = s[u][8 * g + i];
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = NP == 1 ? pack(x[2 * i], x[2 * i + 1]) : cut(x[2 * i], x[2 * i + 1]);
+        p[n] = __builtin_bit_cast(bf16x8, w);
+      }
+    };
     s16x4* const vt = reinterpret_cast<s16x4*>(&vs[0][0] + buffer * kBuffer);
     auto values = [&](int u, int g, int d) {  // operand of 16 tokens and 32 channels
       u32x4 w;
@@ -406,43 +453,24 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
       }
       return w;
     };
-    auto probabilities = [&](int u, int g, bf16x8 (&p)[NP]) {
-      if constexpr (NP == 1) {
-        u32x4 w;
+    // The vector ALU works on the next 16 tokens' probabilities while the matrix cores multiply these.
+    bf16x8 p[2][NP];
+    probabilities(0, 0, p[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack(s[u][8 * g + 2 * i], s[u][8 * g + 2 * i + 1]);
-        p[0] = __builtin_bit_cast(bf16x8, w);
-      } else {
-        float x[8];
+    for (int n16 = 0; n16 < 4; ++n16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = s[u][8 * g + i];
+      for (int d = 0; d < kC; ++d) {
+        u32x4 w = values(n16 >> 1, n16 & 1, d);
+        if constexpr (CAREFUL) {
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-          u32x4 w;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = cut(x[2 * i], x[2 * i + 1]);
-          p[n] = __builtin_bit_cast(bf16x8, w);
+          for (int i = 0; i < 4; ++i) w[i] = even_pair(w[i]);
         }
+        const bf16x8 f = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p[n16 & 1][n], o[d], 0, 0, 0);
       }
-    };
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        bf16x8 p[NP];
-        probabilities(u, g, p);
-#pragma unroll
-        for (int d = 0; d < kC; ++d) {
-          u32x4 w = values(u, g, d);
-          if constexpr (CAREFUL) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = even_pair(w[i]);
-          }
-          const bf16x8 f = __builtin_bit_cast(bf16x8, w);
-#pragma unroll
-          for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p[n], o[d], 0, 0, 0);
-        }
-      }
+      if (n16 < 3) probabilities((n16 + 1) >> 1, (n16 + 1) & 1, p[(n16 + 1) & 1]);
+    }
     if constexpr (CAREFUL) {
       const u32x4* const mine = &vs[buffer][lane * kRowPieces];  // lane i looks at token i
       bool any = false;
@@ -458,7 +486,7 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
           for (int i = 0; i < 16; ++i) p = (tk >> 5) == u && ((tk >> 3 & 3) << 2 | (tk & 3)) == i ? s[u][i] : p;
         p = __shfl(p, r + 32 * (tk >> 2 & 1));
         const uint16_t* const v = reinterpret_cast<const uint16_t*>(&vs[buffer][tk * kRowPieces]);
-        const int vx = D == 128 ? (tk & 3) << 2 : (tk >> 1 & 1) << 2;
+        const int vx = value_xor<D>(tk);
         const bool seen = sees(t0 + tk) && (paged >> (tk >> 4) & 1);
 #pragma unroll
         for (int d = 0; d < kC; ++d)
@@ -540,14 +568,14 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   }
 }
 
-// Parts joined: a wave to a query head of a token.
+// Parts joined: D / 4 lanes to a query head of a token, four channels each.  The lanes weigh a part each, then add the parts.
 template <int D, typename X>
 __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs t) {
   const Args& a = t.a;
-  constexpr int kPer = D / 64;
-  const int lane = threadIdx.x & 63;
-  const uint32_t id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
-  if (id >= (uint32_t)a.T * a.q_heads) return;
+  constexpr int kLanes = D / 4;
+  const int sub = threadIdx.x % kLanes;
+  const uint32_t rows_all = (uint32_t)a.T * a.q_heads;
+  const uint32_t given = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, id = given < rows_all ? given : rows_all - 1;
   const int s = (int)(id / a.q_heads), head = (int)(id % a.q_heads);
   // The sequence of row s: the last one that does not begin behind it.
   int b = 0, end = (int)a.B;
@@ -557,23 +585,40 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs t) {
     else end = mid;
   }
   Item item = {b, 0, run_of(a, b)};
-  if (s < item.run.s0 || s - item.run.s0 >= item.run.n) return;
-  const int row = (s - item.run.s0) * (int)a.share + head % (int)a.share;
-  item.tile = row / kRows;
-  const Steps steps = steps_of(t, item);
-  if (steps.parts == 1) return;
-  const int64_t step = (int64_t)a.T * a.q_heads, ml0 = (int64_t)t.parts * step * D;
-  float m = kLowest, l = 0.0f, o[kPer] = {};
-  for (int p = 0; p < steps.parts; ++p) m = fmaxf(m, a.partial[ml0 + 2 * (p * step + id)]);
-  for (int p = 0; p < steps.parts; ++p) {
-    const float w = exp2_raw(a.partial[ml0 + 2 * (p * step + id)] - m);
-    l = fmaf(w, a.partial[ml0 + 2 * (p * step + id) + 1], l);
+  if (given >= rows_all || s < item.run.s0 || s - item.run.s0 >= item.run.n) return;
+  item.tile = ((s - item.run.s0) * (int)a.share + head % (int)a.share) / kRows;
+  const int parts = steps_of(t, item).parts;
+  if (parts == 1) return;  // its one block has written the result
+  const int64_t step = rows_all;
+  const float* const ml = a.partial + (int64_t)t.parts * step * D + 2 * (int64_t)id;
+  const f32x4* const part = reinterpret_cast<const f32x4*>(a.partial + (int64_t)id * D) + sub;
+  float m = kLowest, l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  for (int first = 0; first < parts; first += kLanes) {
+    const int n = parts - first < kLanes ? parts - first : kLanes;
+    const f32x2 mine = sub < n ? *reinterpret_cast<const f32x2*>(ml + 2 * (first + sub) * step) : f32x2{kLowest, 0.0f};
+    float top = fmaxf(m, mine[0]);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = fmaf(w, a.partial[(p * step + id) * D + kPer * lane + i], o[i]);
+    for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float shrink = exp2_raw(m - top), weight = exp2_raw(mine[0] - top);
+    m = top;
+    l = l * shrink + weight * mine[1];  // of this lane's parts
+    o *= shrink;
+    for (int q = 0; q < n; ++q) {
+      const f32x4 x = part[(first + q) * step * (D / 4)];
+      o += __shfl(weight, q, kLanes) * x;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    store(static_cast<X*>(a.o) + (int64_t)s * a.o_ts + (int64_t)head * a.o_hs + kPer * lane + i, l == 0.0f ? 0.0f : o[i] / l);
+  for (int d = 1; d < kLanes; d <<= 1) l += __shfl_xor(l, d);
+  X* const to = static_cast<X*>(a.o) + (int64_t)s * a.o_ts + (int64_t)head * a.o_hs + 4 * sub;
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = l == 0.0f ? 0.0f : o[i] / l;
+  if constexpr (sizeof(X) == 2)
+    *reinterpret_cast<u32x2*>(to) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
+  else
+    *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
 }
 
 template <int D, typename X>
@@ -583,7 +628,8 @@ hipError_t launch_tiles(const TileArgs& t, int kind, unsigned blocks, hipStream_
                   : tiles_kernel<D, X, kFp8><<<blocks, kThreads, 0, st>>>(t);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || t.parts == 1) return e;
-  join_tiles_kernel<D, X><<<(unsigned)(((int64_t)t.a.T * t.a.q_heads + 3) / 4), 256, 0, st>>>(t);
+  constexpr int kJoined = 256 / (D / 4);  // of a block
+  join_tiles_kernel<D, X><<<(unsigned)(((int64_t)t.a.T * t.a.q_heads + kJoined - 1) / kJoined), 256, 0, st>>>(t);
   return hipGetLastError();
 }
 
@@ -597,7 +643,10 @@ hipError_t launch_run_tiles(const RunArgs& in, hipStream_t st) {
   t.a.T = (int32_t)in.T;
   t.a.sinks = in.sinks > 0x7fffffff ? 0x7fffffff : (int32_t)in.sinks;
   t.a.causal = in.causal;
-  const RunTiles tiles = run_tiles(in.T, in.base.B, in.base.q_heads, in.base.cache.heads, t.a.capacity);
+  RunTiles tiles = run_tiles(in.T, in.base.B, in.base.q_heads, in.base.cache.heads, t.a.capacity);  // as the workspace was sized
+  const int64_t window = in.base.window;
+  if (window > 0 && window < t.a.capacity - kRows - t.a.sinks)
+    tiles = run_tiles(in.T, in.base.B, in.base.q_heads, in.base.cache.heads, window + kRows + t.a.sinks, tiles.parts);
   t.items = tiles.items;
   t.parts = (uint32_t)tiles.parts;
   t.least = (uint32_t)kLeastSteps;
