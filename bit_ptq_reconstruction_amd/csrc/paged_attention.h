@@ -183,8 +183,14 @@ __device__ __forceinline__ unsigned pair_of_codes(unsigned w) {
   return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
 }
 
+// RUN: several blocks read the same tokens one behind the other, so these stay in the cache.
+template <bool RUN, typename T>
+__device__ __forceinline__ T load_once(const char* p) {
+  return RUN ? *reinterpret_cast<const T*>(p) : __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+}
+
 // Keys of one tile as loaded, and as operands of the score product.
-template <int D, int KIND>
+template <int D, int KIND, bool RUN>
 struct Keys {
   static constexpr bool kBytes = KIND != kBf16;
   static constexpr int kLoads = kBytes ? D / 64 : D / 32;
@@ -192,7 +198,7 @@ struct Keys {
   __device__ __forceinline__ void load(const char* tile, uint32_t lane_bytes) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
-      d[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(tile + lane_bytes + 64 * j));
+      d[j] = load_once<RUN, u32x4>(tile + lane_bytes + 64 * j);
   }
   // operand f covers channels channel(f, c) .. + 7
   static __device__ __forceinline__ int channel(int f, int c) {
@@ -219,7 +225,7 @@ struct Keys {
 };
 
 // Channels kE r .. kE r + kE - 1 of one token's value.
-template <int D, int KIND>
+template <int D, int KIND, bool RUN>
 struct Values {
   static constexpr int kE = D / 16;
   static constexpr int kBytes = kE * (KIND != kBf16 ? 1 : 2);
@@ -228,13 +234,13 @@ struct Values {
   __device__ __forceinline__ void load(const char* tile, uint32_t lane_bytes) {
     const char* const p = tile + lane_bytes;
     if constexpr (kWords == 4) {
-      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+      const u32x4 v = load_once<RUN, u32x4>(p);
       d[0] = v[0], d[1] = v[1], d[2] = v[2], d[3] = v[3];
     } else if constexpr (kWords == 2) {
-      const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+      const u32x2 v = load_once<RUN, u32x2>(p);
       d[0] = v[0], d[1] = v[1];
     } else {
-      d[0] = __builtin_nontemporal_load(reinterpret_cast<const unsigned*>(p));
+      d[0] = load_once<RUN, unsigned>(p);
     }
   }
   __device__ __forceinline__ void clear() {
@@ -316,9 +322,15 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
-  uint32_t id = blockIdx.x;
-  const uint32_t q_tile = id % a.q_tiles;
-  id /= a.q_tiles;
+  uint32_t id = blockIdx.x, q_tile;
+  if constexpr (RUN) {  // blocks are dealt out to eight dies in turn: the tiles of a part and head, which read the same, go to one
+    const uint32_t lot = id / (8 * a.q_tiles), in_lot = id % (8 * a.q_tiles);
+    q_tile = in_lot / 8;
+    id = 8 * lot + in_lot % 8;
+  } else {
+    q_tile = id % a.q_tiles;
+    id /= a.q_tiles;
+  }
   const uint32_t h = id % a.heads;
   const uint32_t number = id / a.heads;
   const Part part = find_part<true, RUN>(a, (int)number);
@@ -372,7 +384,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
     const X* row = static_cast<const X*>(a.q) + (int64_t)(run.s0 + token) * a.q_ts + (int64_t)(h * a.share + head) * a.q_hs;
 #pragma unroll
     for (int f = 0; f < kF; ++f) {
-      const X* p = row + Keys<D, KIND>::channel(f, c);
+      const X* p = row + Keys<D, KIND, RUN>::channel(f, c);
       if constexpr (NP == 1) {
         q[f][0] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p));
       } else {
@@ -393,12 +405,12 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
     }
   }
 
-  Keys<D, KIND> k[kU];
-  Values<D, KIND> v[kU][4];
+  Keys<D, KIND, RUN> k[kU];
+  Values<D, KIND, RUN> v[kU][4];
   f32x4 ks[kU], vs[kU];
   float ks1[kU], vs1[kU];  // FP8: of the tile's block
   const uint32_t token_bytes = a.token_stride * kElem;
-  const uint32_t key_lane = r * token_bytes + 16 * c, value_lane = r * Values<D, KIND>::kBytes;
+  const uint32_t key_lane = r * token_bytes + 16 * c, value_lane = r * Values<D, KIND, RUN>::kBytes;
   // Of tile number v: whether there is a token in it that some row does not see.
   const int all_low = RUN && a.window > 0 ? sp.end - a.window : sp.begin, all_high = RUN && a.causal ? sp.end - run.n + 1 : sp.end;
   auto edge = [&](int v) {
@@ -479,7 +491,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
 #pragma unroll
             for (int e = 0; e < kE; ++e)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[e][j] = fmaf(Values<D, KIND>::of(row, kE * (4 * c + j) + e), p, o[e][j]);
+              for (int j = 0; j < 4; ++j) o[e][j] = fmaf(Values<D, KIND, RUN>::of(row, kE * (4 * c + j) + e), p, o[e][j]);
           }
         }
       }
@@ -599,7 +611,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(Args a) {
       for (int e = 0; e < kE; ++e) {
         u32x4 w;
 #pragma unroll
-        for (int z = 0; z < 4; ++z) w[z] = Values<D, KIND>::pair(v[z >> 1][2 * (z & 1)], v[z >> 1][2 * (z & 1) + 1], e);
+        for (int z = 0; z < 4; ++z) w[z] = Values<D, KIND, RUN>::pair(v[z >> 1][2 * (z & 1)], v[z >> 1][2 * (z & 1) + 1], e);
         const bf16x8 vf = __builtin_bit_cast(bf16x8, w);
 #pragma unroll
         for (int n = NV - 1; n >= 0; --n) o[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, p[n], o[e], 0, 0, 0);
@@ -746,7 +758,7 @@ hipError_t launch(Args a, bool split, hipStream_t st) {
   const int64_t each = (int64_t)a.heads * a.q_tiles, round = (int64_t)n * kCUs / each;
   a.few = round - a.B / 2 > round / 2 ? round - a.B / 2 : round / 2;
   if (a.few < 1) a.few = 1;
-  const unsigned blocks = a.parts * a.heads * a.q_tiles;
+  const unsigned each_tile = a.parts * a.heads, blocks = (RUN ? (each_tile + 7) / 8 * 8 : each_tile) * a.q_tiles;
   kernel<<<blocks, 64 * kWaves, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !split) return e;

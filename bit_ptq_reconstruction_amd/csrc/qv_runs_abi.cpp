@@ -15,10 +15,11 @@ bool run_sizes(int64_t T, int64_t B, int64_t max_run, int64_t q_heads, int64_t h
     return false;
   if (max_run == 0) max_run = 1;
   if (B > kMaxInt / q_heads || B * q_heads > kMaxInt / max_run) return false;
-  if (B > 0 && qv::long_runs(max_run, q_heads, heads)) {  // 256 threads to a block, 64 to a row's join
+  if (B > 0 && qv::long_runs(max_run, q_heads, heads, false)) {  // 256 threads to a block, 32 to a row's join
     const qv::RunTiles t = qv::run_tiles(T, B, q_heads, heads, capacity);
-    return T <= kMaxInt / q_heads / 64 && t.items * t.parts <= kMaxThreads / 256 / heads;
+    if (T > kMaxInt / q_heads / 32 || t.items * t.parts > kMaxThreads / 256 / heads) return false;
   }
+  if (qv::long_runs(max_run, q_heads, heads, true)) return true;
   return attention_fits(B, q_heads * max_run, qv::paged_attention_parts(B, q_heads * max_run, heads, capacity));
 }
 

@@ -57,20 +57,27 @@ inline RunTiles run_tiles(int64_t T, int64_t B, int64_t q_heads, int64_t heads, 
   return t;
 }
 
-// Whether a call goes that way.
-constexpr int64_t kFewRows = QV_RUN_FEW_ROWS;
-inline bool long_runs(int64_t max_run, int64_t q_heads, int64_t heads) { return max_run * (q_heads / heads) > kFewRows && max_run > 1; }
+// Whether a call goes that way.  us, few-row kernel and tiles: 16 runs of 5 tokens of 4 query heads over 8192 in bf16 38 and 38, 32 runs
+// of 8 over 4096 73 and 62, one of 48 tokens over 30000 22 and 41; over 8-bit caches, which the tiles convert ahead of their
+// products, 29 to 32 and 53 to 55, 51 to 57 and 80 to 84, 21 to 23 and 51 to 53, one of 16 x 4 rows over 30000 41 to 46 and 55 to 59.
+inline bool long_runs(int64_t max_run, int64_t q_heads, int64_t heads, bool bytes) {
+  return max_run > 1 && max_run * (q_heads / heads) > (bytes ? QV_RUN_FEW_ROWS_8BIT : QV_RUN_FEW_ROWS);
+}
 
-// Bytes of partial results that the launch may write.
+// Bytes of partial results that the launch may write, whatever the cache holds.
 inline int64_t run_attention_bytes(int64_t T, int64_t B, int64_t max_run, int64_t q_heads, int64_t heads, int64_t head_dim,
                                    int64_t capacity) {
   if (max_run == 0 || B == 0) return 0;
-  if (long_runs(max_run, q_heads, heads)) {
+  int64_t rows = 0;
+  if (long_runs(max_run, q_heads, heads, false)) {
     const RunTiles t = run_tiles(T, B, q_heads, heads, capacity);
-    return t.parts > 1 ? t.parts * T * q_heads * (head_dim + 2) * 4 : 0;
+    if (t.parts > 1) rows = t.parts * T * q_heads;
   }
-  const AttentionParts p = paged_attention_parts(B, q_heads * max_run, heads, capacity);
-  return p.split ? p.most * q_heads * max_run * (head_dim + 2) * 4 : 0;
+  if (!long_runs(max_run, q_heads, heads, true)) {
+    const AttentionParts p = paged_attention_parts(B, q_heads * max_run, heads, capacity);
+    if (p.split && p.most * q_heads * max_run > rows) rows = p.most * q_heads * max_run;
+  }
+  return rows * (head_dim + 2) * 4;
 }
 
 }  // namespace qv

@@ -353,22 +353,32 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
     float top = -INFINITY;
     const u32x4* const kt = &ks[0][0] + buffer * kBuffer;
     f32x16 acc[2] = {f32x16{}, f32x16{}};
+    // Keys are read a group of operands ahead of the products.
+    constexpr int kGroup = D == 64 && NP == 1 ? 4 : 2;
+    bf16x8 f[2][kGroup][2];
+    auto read_keys = [&](int group) {
 #pragma unroll
-    for (int k = 0; k < kK; ++k)
+      for (int k = 0; k < kGroup; ++k)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bf16x8 f = __builtin_bit_cast(bf16x8, kt[k_at[k] + 32 * u * kRowPieces]);
+        for (int u = 0; u < 2; ++u)
+          f[group & 1][k][u] = __builtin_bit_cast(bf16x8, kt[k_at[group * kGroup + k] + 32 * u * kRowPieces]);
+    };
+    // While matrix instructions are to be issued the wave goes before the one that shares its SIMD.
+    if constexpr (KIND == kBf16) __builtin_amdgcn_s_setprio(1);
+    read_keys(0);
 #pragma unroll
-        for (int n = NP - 1; n >= 0; --n) acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k][n], acc[u], 0, 0, 0);
-      }
-    if constexpr (NP == 1) {  // six reads ahead
-      __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+    for (int group = 0; group < kK / kGroup; ++group) {
+      if (group + 1 < kK / kGroup) read_keys(group + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      }
+      for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int n = NP - 1; n >= 0; --n)
+            acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[group & 1][k][u], q[group * kGroup + k][n], acc[u], 0, 0, 0);
     }
+    if constexpr (KIND == kBf16) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -455,22 +465,31 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
     };
     // The vector ALU works on the next 16 tokens' probabilities while the matrix cores multiply these.
     bf16x8 p[2][NP];
+    u32x4 w[2][kC];
+    auto read_values = [&](int n16) {
+#pragma unroll
+      for (int d = 0; d < kC; ++d) w[n16 & 1][d] = values(n16 >> 1, n16 & 1, d);
+    };
+    read_values(0);
+    __builtin_amdgcn_sched_barrier(0);
     probabilities(0, 0, p[0]);
+    if constexpr (KIND == kBf16) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int n16 = 0; n16 < 4; ++n16) {
+      if (n16 < 3) read_values(n16 + 1);
 #pragma unroll
       for (int d = 0; d < kC; ++d) {
-        u32x4 w = values(n16 >> 1, n16 & 1, d);
         if constexpr (CAREFUL) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = even_pair(w[i]);
+          for (int i = 0; i < 4; ++i) w[n16 & 1][d][i] = even_pair(w[n16 & 1][d][i]);
         }
-        const bf16x8 f = __builtin_bit_cast(bf16x8, w);
+        const bf16x8 f = __builtin_bit_cast(bf16x8, w[n16 & 1][d]);
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p[n16 & 1][n], o[d], 0, 0, 0);
       }
       if (n16 < 3) probabilities((n16 + 1) >> 1, (n16 + 1) & 1, p[(n16 + 1) & 1]);
     }
+    if constexpr (KIND == kBf16) __builtin_amdgcn_s_setprio(0);
     if constexpr (CAREFUL) {
       const u32x4* const mine = &vs[buffer][lane * kRowPieces];  // lane i looks at token i
       bool any = false;

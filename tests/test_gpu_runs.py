@@ -404,9 +404,9 @@ def runs64(Q, starts, cache, table, lens, window, sinks, causal, scale, max_run=
     return out
 
 
-def rounds(max_run, share, xt):
+def rounds(max_run, share, xt, kind="bf16"):
     """Whether the probabilities of such a call are rounded to bf16."""
-    return xt == "bf16" and max_run > 1 and max_run * share > 32
+    return xt == "bf16" and max_run > 1 and max_run * share > (32 if kind == "bf16" else 64)
 
 
 def check(O, expect, xt, rounded, label=""):
@@ -482,7 +482,7 @@ def test_run_attention(qv, dev, runs, before, heads, share, dim, page, window, s
     Q = (2 * torch.randn((sum(runs) + 2, heads * share, dim), generator=g)).to(DT[xt])
     starts = sums(runs)
     O = attend(qv, dev, Q.to(dev), starts, max(runs), cache, table, lens, window, sinks, causal, pad=8)
-    check(O, runs64(Q, starts, cache, table, lens, window, sinks, causal, dim ** -0.5), xt, rounds(max(runs), share, xt))
+    check(O, runs64(Q, starts, cache, table, lens, window, sinks, causal, dim ** -0.5), xt, rounds(max(runs), share, xt, kind))
     assert bool(torch.isnan(O[starts[-1]:].float()).all())  # rows that no sequence has
     if max(runs) == 1 and starts[-1] == len(runs):  # single tokens without starts
         again = attend(qv, dev, Q[:len(runs)].to(dev), None, 1, cache, table, lens, window, sinks, causal, pad=8)
@@ -558,7 +558,7 @@ def test_what_a_row_does_not_see(qv, dev, xt, kind, dim, run, share, window):
         if seen:
             assert not bool(torch.isfinite(O[i]).all(-1).any()), f"row {i} sees {seen}"
         else:
-            rounded = rounds(run, share, xt)
+            rounded = rounds(run, share, xt, kind)
             check(O[i:i + 1], [x[i:i + 1] for x in clean], xt, rounded, f"row {i}")
 
 
