@@ -11,7 +11,11 @@
 // A wave owns a block of one head: it finds the run of the call's tokens that lie in the block, their maximum, the scale, and
 // writes.  So no two waves touch a block and nothing is atomic.  The wave of a block's first token in the call (its leader)
 // does this; waves look through a window of tokens for leaders.  A lane holds 8 low and 8 high channels of one token, both
-// sides of its pairs.
+// sides of its pairs.  The first tokens of a block (32 of 64 channels or 16 of 128) stay in registers between maximum and codes;
+// their loads go out before the block's page is known.
+//
+// Bound by memory for prompts: 10992 tokens of 48 heads of 64 in blocks of 32 (116 MB) take 31 us, 3.7 TB/s (read twice and a
+// token at a time it took 41).  One token of each of 24 sequences takes 6.0 us: a launch and the chain place -> page -> scale -> code.
 #include "append_rows.h"
 
 namespace qv {
@@ -49,26 +53,44 @@ struct Part {
   }
 };
 
-// Cosines and sines of token t for the lane's pairs; false: a position outside the tables.
+// Whether token t's position lies in the tables, and its place on the lane's axis.
 template <int D>
-__device__ __forceinline__ bool angles(const Args& a, const Part<D>& part, int64_t t, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ bool known_place(const Args& a, const Part<D>& part, int64_t t, int* p) {
+  *p = 0;
   if (!a.cos) return true;
-  int p;
-  bool known;
   if (a.position) {
     const int p0 = a.position[t * a.axes], p1 = a.position[t * a.axes + a.axes - 1];
-    known = p0 >= 0 && p0 < a.places && p1 >= 0 && p1 < a.places;
-    p = part.axis ? p1 : p0;
-  } else {
-    p = a.index[t];
-    known = p >= 0 && p < a.places;
+    *p = part.axis ? p1 : p0;
+    return p0 >= 0 && p0 < a.places && p1 >= 0 && p1 < a.places;
   }
-  if (known) {
-    load8(a.cos + (int64_t)p * part.half + part.j, c);
-    load8(a.sin + (int64_t)p * part.half + part.j, s);
-  }
-  return known;
+  *p = a.index[t];
+  return *p >= 0 && *p < a.places;
 }
+
+// The lane's channels of a row as they lie in memory.
+template <typename X>
+struct Raw {
+  u32x4 d[sizeof(X)];  // low channels, then high ones
+  __device__ __forceinline__ void load(const X* row, int low, int high) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(X) / 2; ++i) {
+      d[i] = reinterpret_cast<const u32x4*>(row + low)[i];
+      d[sizeof(X) / 2 + i] = reinterpret_cast<const u32x4*>(row + high)[i];
+    }
+  }
+  __device__ __forceinline__ void get(int first, float (&v)[8]) const {
+    if constexpr (sizeof(X) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bits_float(d[first][i] << 16);
+        v[2 * i + 1] = bits_float(d[first][i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = bits_float(d[2 * first + (i >> 2)][i & 3]);
+    }
+  }
+};
 
 // The scale by which a largest magnitude (its bits, finite) is at most 448 = 1.75 * 2^8.
 __device__ __forceinline__ float scale_of(uint32_t top) {
@@ -110,6 +132,7 @@ template <int D, typename X>
 struct Append {
   static constexpr int kParts = D / 16;        // lanes of a token
   static constexpr int kStep = 64 / kParts;    // tokens at a time
+  static constexpr int kKept = 2;              // steps that stay in registers
   const Args& a;
   const int lane;
   const Part<D> part;
@@ -121,61 +144,89 @@ struct Append {
 
   // Whether token t is the first of the call in its block.
   __device__ __forceinline__ bool leads(int64_t t) const {
+    if (!a.seq) return true;  // one token to a sequence
     const uint32_t place = (uint32_t)a.index[t];
     return t == 0 || place % (uint32_t)a.block == 0 || sequence(t - 1) != sequence(t) || (uint32_t)a.index[t - 1] + 1 != place;
   }
 
-  __device__ __forceinline__ bool load(const Rows& src, int head, bool turned, int64_t t, float (&lo)[8], float (&hi)[8]) const {
-    const X* const x = static_cast<const X*>(src.data) + t * src.ts + head * src.hs;
-    load8(x + part.low, lo);
-    load8(x + part.high, hi);
-    float c[8], s[8];
-    const bool known = angles(a, part, t, c, s);
-    if (a.cos && known && turned) turn(lo, hi, c, s);
+  __device__ __forceinline__ const X* row(const Rows& src, int head, int64_t t) const {
+    return static_cast<const X*>(src.data) + t * src.ts + head * src.hs;
+  }
+  // Token t's channels, turned if they are a key's or query's; false: its position is unknown.
+  __device__ __forceinline__ bool values(const Raw<X>& raw, bool turned, int64_t t, float (&lo)[8], float (&hi)[8]) const {
+    raw.get(0, lo);
+    raw.get(1, hi);
+    int p;
+    const bool known = known_place(a, part, t, &p);
+    if (a.cos && known && turned) {
+      float c[8], s[8];
+      load8(a.cos + (int64_t)p * part.half + part.j, c);
+      load8(a.sin + (int64_t)p * part.half + part.j, s);
+      turn(lo, hi, c, s);
+    }
     return known;
   }
 
-  // The block that token t leads, for one head of the keys or values.
+  // The block that token t leads (if it does), for one head of the keys or values.
   __device__ __forceinline__ void block(int64_t t, bool key, int head) const {
+    const Rows& src = key ? a.k : a.v;
+    const uint32_t mine = lane / kParts;
+    Raw<X> raw[kKept];  // on their way while the place is found
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      const int64_t s = t + mine + i * kStep;
+      if (s < a.T) raw[i].load(row(src, head, s), part.low, part.high);
+    }
+    // Places and sequences of this token and those behind it, a lane each.
+    const int64_t mine_t = t + lane < a.T ? t + lane : a.T - 1;
+    const int32_t my_place = a.index[mine_t], my_seq = a.seq ? a.seq[mine_t] : 0;
+    if (!leads(t)) return;
     const uint32_t size = (uint32_t)a.block;
-    const int place = a.index[t];
-    const int64_t seq = sequence(t);
+    const int place = __builtin_amdgcn_readfirstlane(my_place);
+    const int64_t seq = a.seq ? (int64_t)__builtin_amdgcn_readfirstlane(my_seq) : t;
     if (place < 0 || seq < 0 || seq >= a.num_seqs) return;
     const uint32_t entry = (uint32_t)place / (uint32_t)a.page_size, slot = (uint32_t)place % (uint32_t)a.page_size;
     if (entry >= (uint32_t)a.max_pages) return;
     const int64_t page = a.table[seq * a.ld_table + entry];
-    if (page < 0 || page >= a.num_pages) return;
     const uint32_t at = slot % size, most = size - at;
+
+    uint32_t n = 1;  // tokens of the call that lie in the block
+    if (a.seq) {
+      const uint32_t ahead = lane;
+      uint64_t missing = ~__ballot(ahead < most && t + lane < a.T && my_seq == seq && (uint32_t)my_place == (uint32_t)place + ahead);
+      n = missing ? __builtin_ctzll(missing) : 64;
+      while (!missing) {
+        const uint32_t j = n + lane;
+        const bool ok = j < most && t + j < a.T && a.seq[t + j] == seq && (uint32_t)a.index[t + j] == (uint32_t)place + j;
+        missing = ~__ballot(ok);
+        n += missing ? __builtin_ctzll(missing) : 64;
+      }
+    }
+    if (page < 0 || page >= a.num_pages) return;
     float* const held = (key ? a.ks : a.vs) + (page * a.heads + head) * (a.page_size / size) + slot / size;
     const float before = at ? *held : 0.0f;
 
-    uint32_t n = 0;  // tokens of the call that lie in the block
-    for (;;) {
-      const uint32_t j = n + lane;
-      const bool ok = j < most && t + j < a.T && sequence(t + j) == seq && (uint32_t)a.index[t + j] == (uint32_t)place + j;
-      const uint64_t missing = ~__ballot(ok);
-      n += missing ? __builtin_ctzll(missing) : 64;
-      if (missing) break;
-    }
-
-    const Rows& src = key ? a.k : a.v;
-    const uint32_t mine = lane / kParts;
-    float lo[8], hi[8];
-    bool stored = false;
     uint32_t top = 0;
-    auto largest = [&]() {
+    auto largest = [&](const float (&x)[8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t l = float_bits(lo[i]) & 0x7FFFFFFFu, h = float_bits(hi[i]) & 0x7FFFFFFFu;
-        if (l < kInfinity && l > top) top = l;
-        if (h < kInfinity && h > top) top = h;
+        const uint32_t b = float_bits(x[i]) & 0x7FFFFFFFu;
+        if (b < kInfinity && b > top) top = b;
       }
     };
-    for (uint32_t j = kStep + mine; j < n; j += kStep)
-      if (load(src, head, key, t + j, lo, hi)) largest();
-    if (mine < n) {  // these stay in registers
-      stored = load(src, head, key, t + mine, lo, hi);
-      if (stored) largest();
+    float lo[kKept][8], hi[kKept][8];
+    bool stored[kKept];
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      const uint32_t j = mine + i * kStep;
+      stored[i] = j < n && values(raw[i], key, t + j, lo[i], hi[i]);
+      if (stored[i]) largest(lo[i]), largest(hi[i]);
+    }
+    for (uint32_t j = kKept * kStep + mine; j < n; j += kStep) {  // these are read again below
+      Raw<X> x;
+      float l[8], h[8];
+      x.load(row(src, head, t + j), part.low, part.high);
+      if (values(x, key, t + j, l, h)) largest(l), largest(h);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
@@ -184,16 +235,21 @@ struct Append {
     const float inverse = 1.0f / s;
 
     char* const start = (key ? a.kp : a.vp) + page * a.page_stride + head * a.head_stride + (int64_t)(slot - at) * a.token_stride;
-    if (stored) {
-      char* const to = start + (int64_t)(at + mine) * a.token_stride;
-      store8(to + part.low, lo, s, inverse, exact);
-      store8(to + part.high, hi, s, inverse, exact);
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      if (!stored[i]) continue;
+      char* const to = start + (int64_t)(at + mine + i * kStep) * a.token_stride;
+      store8(to + part.low, lo[i], s, inverse, exact);
+      store8(to + part.high, hi[i], s, inverse, exact);
     }
-    for (uint32_t j = kStep + mine; j < n; j += kStep) {
-      if (!load(src, head, key, t + j, lo, hi)) continue;
+    for (uint32_t j = kKept * kStep + mine; j < n; j += kStep) {
+      Raw<X> x;
+      float l[8], h[8];
+      x.load(row(src, head, t + j), part.low, part.high);
+      if (!values(x, key, t + j, l, h)) continue;
       char* const to = start + (int64_t)(at + j) * a.token_stride;
-      store8(to + part.low, lo, s, inverse, exact);
-      store8(to + part.high, hi, s, inverse, exact);
+      store8(to + part.low, l, s, inverse, exact);
+      store8(to + part.high, h, s, inverse, exact);
     }
     if (at && before != s) {
       const float ratio = before / s;
@@ -205,7 +261,9 @@ struct Append {
   __device__ __forceinline__ void query(int64_t t, int head) const {
     if (head >= a.q_heads) return;
     float lo[8], hi[8];
-    if (!load(a.q, head, true, t, lo, hi)) {
+    Raw<X> x;
+    x.load(row(a.q, head, t), part.low, part.high);
+    if (!values(x, true, t, lo, hi)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) lo[i] = hi[i] = __builtin_nanf("");
     }
@@ -224,8 +282,12 @@ __global__ __launch_bounds__(kThreads) void append_fp8_kernel(Args a) {
     const uint32_t end = first + a.window < a.count ? first + a.window : a.count;
     const bool key = which < (uint32_t)a.heads;
     const int head = key ? which : which - a.heads;
-    const bool leads = first + append.lane < end && append.leads(a.first + first + append.lane);
-    for (uint64_t left = __ballot(leads); left; left &= left - 1) append.block(a.first + first + __builtin_ctzll(left), key, head);
+    if (a.window == 1) {
+      append.block(a.first + first, key, head);
+    } else {
+      const bool leads = first + append.lane < end && append.leads(a.first + first + append.lane);
+      for (uint64_t left = __ballot(leads); left; left &= left - 1) append.block(a.first + first + __builtin_ctzll(left), key, head);
+    }
   } else if (wave - a.kv_waves < a.q_waves) {
     const uint32_t id = wave - a.kv_waves;
     append.query(a.first + id / a.q_groups, id % a.q_groups * Append<D, X>::kStep + append.lane / Append<D, X>::kParts);
@@ -268,12 +330,12 @@ hipError_t launch_kv_append_fp8(const AppendArgs& in, hipStream_t st) {
   const int64_t step = 64 / (c.head_dim / 16);
   a.q_groups = (uint32_t)((in.q_heads + step - 1) / step);
   // A wave for each token while that does not fill the chip, so that single tokens of many sequences go side by side; then
-  // windows of up to 16, since only one wave in a block's tokens finds a leader.
+  // windows of up to a block (and 64), since only one wave in a block's tokens finds a leader.
   a.window = 1;
-  while (a.window < 16 && in.T * 2 * c.heads / a.window > 8192) a.window *= 2;
+  while (a.window < 64 && 2 * a.window <= (uint32_t)a.block && in.T * 2 * c.heads / a.window > 8192) a.window *= 2;
   // A launch counts its waves in 32 bits; longer runs of tokens go in several.
   const int64_t per_token = 2 * c.heads + a.q_groups;
-  const int64_t most = (int64_t{1} << 25) / per_token / 16 * 16 > 0 ? (int64_t{1} << 25) / per_token / 16 * 16 : 16;
+  const int64_t most = (int64_t{1} << 25) / per_token / 64 * 64 > 0 ? (int64_t{1} << 25) / per_token / 64 * 64 : 64;
   for (int64_t t = 0; t < in.T; t += most) {
     a.first = t;
     a.count = (uint32_t)(in.T - t < most ? in.T - t : most);

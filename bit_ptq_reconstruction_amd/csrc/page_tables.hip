@@ -6,9 +6,12 @@
 // a sum over the sequences gives the rows, a second one (of those that fit) the pages, and each row finds its sequence by
 // bisection of the first sum in LDS.
 //
-// Few rows: one block does everything.  Many: blocks take slices of the rows, each works the sums out by itself (8 bytes a
-// sequence), and a second launch of one block writes what may lie in the inputs' place (lengths, count) and the rest of the
-// state.
+// Few rows: one block does everything.  Many: blocks take slices of the rows and each works the sums out by itself (8 bytes a
+// sequence).  The first one also writes the sequences' state; where that lies in the inputs' place (lengths, count), which the
+// other blocks read, a second launch of one block does.
+//
+// 24 sequences of one new token take 4.3 us, of which a launch is 2.5; 300 with prompts of up to 1374 tokens (176433 rows of 16
+// bytes) 6.9, in place 11.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,7 +31,7 @@ struct Args {
   int64_t num_free, ld_table;
   uint32_t B, T, page_size, capacity;
   uint32_t slice;   // rows of a block
-  int32_t rows, state;  // whether this launch writes the rows, and the sequences' state
+  int32_t rows, state;  // whether this launch writes the rows, and its first block the sequences' state
 };
 
 // Sums of numbers >= 0 that stay at the largest one.
@@ -75,6 +78,7 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(Args a) {
   uint32_t rows = 0, asked = 0;  // of the chunks before
   __shared__ uint32_t granted;
   if (threadIdx.x == 0) granted = 0;
+  const bool state = a.state && blockIdx.x == 0;
 
   for (uint32_t chunk = 0; chunk == 0 || chunk < a.B; chunk += kThreads) {
     const uint32_t b = chunk + threadIdx.x;
@@ -94,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(Args a) {
     if (threadIdx.x == kThreads - 1) starts[kThreads] = end;
     len[threadIdx.x] = l;
     from[threadIdx.x] = why ? kRefused : count - 1 - before + held;
-    if (a.state && live) {
+    if (state && live) {
       a.starts[b] = cut(at);
       if (b == a.B - 1) a.starts[a.B] = cut(end);
       a.lens_out[b] = (int32_t)(why ? l : l + n);
@@ -138,7 +142,7 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(Args a) {
     rows = add(rows, all_rows);
     asked = add(asked, all_pages);
   }
-  if (a.state) {
+  if (state) {
     __syncthreads();
     if (threadIdx.x == 0) {
       *a.free_left = (int32_t)(count - granted);
@@ -174,10 +178,10 @@ hipError_t launch_page_tables(const TablesArgs& in, hipStream_t st) {
   if (in.T > 2 * kThreads) {
     const uint32_t blocks = in.T > 1024 * kThreads ? 1024 : (uint32_t)((in.T + kThreads - 1) / kThreads);
     a.slice = (uint32_t)((in.T + blocks - 1) / blocks);
-    a.state = 0;
+    a.state = in.lens_out != in.lens && in.free_left != in.free_count;
     tables_kernel<<<blocks, kThreads, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.state) return e;
     a.rows = 0;
     a.state = 1;
   }

@@ -44,6 +44,7 @@ typedef enum {
  *   status      [B] int32 out: qv_run_status.  A sequence is refused as a whole: it takes no pages and keeps its length, but
  *               its rows stay its own.  Sequences are served in order: one that lacks pages has asked for them all the same, so
  *               that no later one that needs a page gets any.  A sequence without new tokens is never refused for pages or rows.
+ * Outputs other than those two, and the table, do not overlap the inputs or each other.
  * The page of a place before lens[b] is read from the table.  T = 0 is accepted with null outputs of [T].  T <= 2^31 - 1.
  */
 qv_status qv_page_tables(const int32_t* runs, const int32_t* lens, int64_t B, int64_t page_size, const int32_t* free_pages,
