@@ -7,6 +7,7 @@ namespace qv {
 
 hipError_t launch_run_attention(const RunArgs& in, hipStream_t st) {
   if (long_runs(in.max_run, in.base.q_heads, in.base.cache.heads, in.base.cache.dtype != QV_KV_BF16)) return launch_run_tiles(in, st);
+  if (!in.starts && in.sinks == 0) return launch_paged_attention(in.base, st);  // a single token sees no token behind itself
   bool split;
   Args a = arguments(in.base, in.max_run, &split);
   a.starts = in.starts;

@@ -1,0 +1,121 @@
+"""StreamBlock's runs of tokens, shared pages, window and first tokens: tables, append and attention together."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_decode import BF, dev, gen, qv, turn32  # noqa: E402,F401
+from test_gpu_runs import held, runs64, sums  # noqa: E402
+from test_gpu_stream import make, places, rows, weights  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attended(block, b, runs, before, causal, window, sinks):
+    """The attention of a call from the block's own queries and cache, in 64 bits, against what the block has formed."""
+    T = sum(runs)
+    Q = b["q"][:T].cpu()
+    lens = [n + m for n, m in zip(runs, before)]
+    o, mag, root = runs64(Q, sums(runs), block.cache, block.table.cpu(), lens, window, sinks, causal, block.dim ** -0.5)
+    err = (b["o"][:T].double().cpu() - o).abs()
+    # probabilities and results in bf16, 2^-8 each; the rest of test_gpu_runs' bound
+    worst = (err / ((1e-5 + BF) * mag + 1.01 * BF * o.abs() + 1e-38)).max().item()
+    assert worst <= 1.0, f"{worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("cache", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("window,sinks,causal", [(0, 0, True), (0, 0, False), (20, 3, True)])
+def test_runs_of_many_sequences(qv, dev, weights, cache, window, sinks, causal):
+    """Prompts, chunks and single tokens of three sequences over shared pages: keys, values and attention of every call, and the
+    same outputs where each sequence has pages of its own."""
+    calls = [([30, 0, 47], causal), ([1, 64, 1], True), ([17, 5, 0], causal)]
+    kw = dict(sequences=3, capacity=128, frame_tokens=90, int8_cache=cache == "int8", fp8_cache=cache == "fp8", window=window,
+              sinks=sinks)
+    shared, own = make(qv, dev, weights, pages=16, **kw), make(qv, dev, weights, **kw)
+    g = gen(7)
+    before = [0, 0, 0]
+    for runs, how in calls:
+        T = sum(runs)
+        x, at = rows(T, g, dev), places(T, g, dev)
+        out = shared.take_runs(x, runs, at, how)
+        assert torch.equal(out, own.take_runs(x, runs, at, how)) and bool(torch.isfinite(out.float()).all())
+        qkv = shared.frame["qkv"][:T].cpu().view(T, 3, 16, 64)
+        turned = turn32(qkv[:, 0], shared.cos.cpu(), shared.sin.cpu(), at.cpu(), 2).to(torch.bfloat16)
+        assert torch.equal(shared.frame["q"][:T].cpu(), turned)
+        attended(shared, shared.frame, runs, before, how, window, sinks)
+        if cache == "bf16":
+            k = turn32(qkv[:, 1], shared.cos.cpu(), shared.sin.cpu(), at.cpu(), 2).to(torch.bfloat16)
+            row = 0
+            for s, n in enumerate(runs):
+                t = torch.arange(before[s], before[s] + n)
+                page, slot = shared.table[s].cpu().long()[t // 16], t % 16
+                assert torch.equal(shared.cache.k_pages.cpu()[page, :, slot], k[row:row + n])
+                assert torch.equal(shared.cache.v_pages.cpu()[page, :, slot], qkv[row:row + n, 2])
+                row += n
+        before = [n + m for n, m in zip(runs, before)]
+        assert shared.lens.tolist() == own.lens.tolist() == before == shared.held
+        assert int(shared.count) == shared.left == 16 - sum(-(-n // 16) for n in before)
+    x = rows(3, g, dev)
+    for block in (shared, own):
+        block.position.zero_()
+    out = shared.step(x)
+    assert torch.equal(out, own.step(x))
+    attended(shared, shared.one, [1, 1, 1], before, True, window, sinks)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_replayed_steps_over_shared_pages(qv, dev, weights, cache):
+    """A captured step takes pages as its sequences grow: replays, with the host's own work between them, give what eager steps
+    give."""
+    kw = dict(sequences=2, capacity=64, frame_tokens=40, pages=7, fp8_cache=cache == "fp8", window=24, sinks=2)
+    eager, graphed = make(qv, dev, weights, **kw), make(qv, dev, weights, **kw)
+    g = gen(4)
+    x0, at = rows(40, g, dev), places(40, g, dev)
+    xs = [rows(2, g, dev) for _ in range(18)]
+    for block in (eager, graphed):
+        block.take_runs(x0, [30, 10], at)
+        block.step(xs[0])
+    x = xs[1].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = graphed.step(x)
+    for i in range(1, 18):
+        x.copy_(xs[i])
+        graphed.reserve()
+        graph.replay()
+        assert torch.equal(out, eager.step(xs[i])), i
+        assert graphed.lens.tolist() == graphed.held == eager.held and int(graphed.count) == graphed.left == eager.left
+    assert eager.held == [48, 28] and eager.left == 7 - 3 - 2
+
+
+def test_pages_come_back(qv, dev, weights):
+    """What passes the pool, or a sequence's room, is refused before anything is launched; a sequence that ends gives its pages
+    back."""
+    block = make(qv, dev, weights, sequences=3, capacity=64, frame_tokens=64, pages=4)
+    g = gen(2)
+    feed = lambda runs: block.take_runs(rows(sum(runs), g, dev), runs, places(sum(runs), g, dev))
+    feed([33, 0, 5])  # four pages
+    state = lambda: (block.lens.tolist(), block.held, int(block.count), block.left, block.table.tolist())
+    full = state()
+    for runs in ([0, 1, 0], [16, 0, 0], [0, 0, 12]):
+        with pytest.raises(ValueError, match="1 pages needed, 0 of 4 are free"):
+            feed(runs)
+    with pytest.raises(ValueError, match="sequence 0 holds 33 tokens .* 32 more in 64"):
+        feed([32, 0, 0])
+    with pytest.raises(ValueError, match="pages needed"):
+        block.step(rows(3, g, dev))
+    with pytest.raises(ValueError, match="pages needed"):
+        block.take_frame(rows(3, g, dev), 1, places(3, g, dev))
+    assert state() == full
+    block.end(0)
+    assert block.held == [0, 0, 5] and int(block.count) == block.left == 3
+    feed([0, 33, 11])
+    block.take_frame(rows(15, g, dev), 1, places(15, g, dev))
+    taken = block.table[1].tolist()[:3] + block.table[2].tolist()[:1]
+    assert sorted(taken) == [0, 1, 2, 3] and block.lens.tolist() == [0, 48, 16]
+    for runs in ([1, 2], [1, 2, -1], [1, 1, 1]):
+        with pytest.raises(ValueError, match="runs"):
+            block.take_runs(rows(4, g, dev), runs, places(4, g, dev))
+    with pytest.raises(ValueError, match="65 tokens, the block was made for"):
+        block.take_runs(rows(65, g, dev), [65, 0, 0], places(65, g, dev))
+    with pytest.raises(ValueError, match="int8 or FP8"):
+        make(qv, dev, weights, int8_cache=True, fp8_cache=True)
