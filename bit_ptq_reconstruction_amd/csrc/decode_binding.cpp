@@ -49,6 +49,7 @@ const char* type_name(at::ScalarType t) {
     case at::kHalf: return "float16";
     case at::kDouble: return "float64";
     case at::kFloat8_e4m3fn: return "float8_e4m3fn";
+    case at::kFloat8_e5m2: return "float8_e5m2";
     default: return c10::toString(t);
   }
 }
