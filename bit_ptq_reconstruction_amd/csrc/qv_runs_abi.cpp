@@ -11,7 +11,8 @@ namespace {
 // Whether a batch's sizes are ones that the kernels take.
 bool run_sizes(int64_t T, int64_t B, int64_t max_run, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t capacity) {
   if (T < 0 || T > kMaxInt || B < 0 || max_run < 0 || max_run > T || heads <= 0 || heads > 65536 || q_heads <= 0 ||
-      q_heads > 65536 || q_heads % heads != 0 || (head_dim != 64 && head_dim != 128) || capacity < 0 || capacity > kMaxInt)
+      q_heads > 65536 || q_heads % heads != 0 || (head_dim != 64 && head_dim != 128) || capacity < 0 ||
+      capacity > kMaxInt - qv::kTokensPerStep)  // the end of a step is counted in 31 bits
     return false;
   if (max_run == 0) max_run = 1;
   if (B > kMaxInt / q_heads || B * q_heads > kMaxInt / max_run) return false;

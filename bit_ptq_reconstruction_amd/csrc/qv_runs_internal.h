@@ -50,7 +50,7 @@ inline RunTiles run_tiles(int64_t T, int64_t B, int64_t q_heads, int64_t heads, 
   const int64_t steps = seen / kTokensPerStep + 1, blocks = t.items * heads, most = steps / kLeastSteps;
   int64_t best = 0;
   for (int64_t p = 1; p <= room && p <= most && (p == 1 || blocks * (p - 1) < 8 * kTileCUs); ++p) {
-    const int64_t on_a_cu = (blocks * p + kTileCUs - 1) / kTileCUs, each = (steps + p - 1) / p + 6;
+    const int64_t on_a_cu = (blocks * p + kTileCUs - 1) / kTileCUs, each = (uint32_t)(steps + p - 1) / (uint32_t)p + 6;
     const int64_t cost = 2 * on_a_cu * each + (on_a_cu == 1 ? each : 0) + (p > 1 ? 2 * p + 12 : 0);
     if (p == 1 || cost < best) best = cost, t.parts = p;
   }

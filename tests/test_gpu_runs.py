@@ -630,3 +630,124 @@ def test_far_pages(qv, dev, run):
     assert torch.equal(far, near)
     check(near, runs64(Q.cpu(), [0, run], small, table - (pages - need), [n], 0, 0, True, dim ** -0.5), "bf16",
           rounds(run, 1, "bf16"))
+
+
+@pytest.mark.parametrize("scale", [-0.4, 0.0, 3.0])
+@pytest.mark.parametrize("xt,run", [("bf16", 4), ("bf16", 90), ("fp32", 70)])
+def test_scales(qv, dev, scale, xt, run):
+    """Scales of any sign, zero (the plain mean of what a row sees), and ones that leave a row one or two tokens."""
+    g = gen(run)
+    lens = [run + 100, run]
+    table, pages = shuffled_table(lens, 16, g)
+    cache = make(qv, dev, pages, 2, 16, 64, "bf16", 3)
+    Q = torch.randn((2 * run, 2, 64), generator=g).to(DT[xt])
+    starts = sums([run] * 2)
+    O = attend(qv, dev, Q.to(dev), starts, run, cache, table, lens, 40, 2, scale=scale)
+    # scores of up to about 150 bits lose four roundings of 150 * 2^-24 each: ten times the bound of scores below 17
+    expect = runs64(Q, starts, cache, table, lens, 40, 2, True, scale)
+    expect[1] = expect[1] * 10
+    check(O, expect, xt, rounds(run, 1, xt))
+
+
+class Serve:
+    """Tables, append and attention of two calls of runs, as a serving loop makes them, into the same buffers."""
+
+    def __init__(self, qv, dev, kind, run):
+        self.qv, g = qv, gen(run)
+        self.runs = torch.tensor([run, 0, 3], dtype=torch.int32, device=dev)
+        self.T, self.run, H, D = run + 3, run, 2, 64
+        self.cache = make(qv, dev, 80, H, 16, D, kind, 5)
+        self.table = torch.full((3, 40), -1, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(3, dtype=torch.int32, device=dev)
+        self.free = torch.randperm(80, generator=g).to(torch.int32).to(dev)
+        self.count = torch.full((1,), 80, dtype=torch.int32, device=dev)
+        e = lambda n, t=torch.int32: torch.empty(n, dtype=t, device=dev)
+        self.out = [e(4), e(self.T), e(self.T), e(self.T, torch.int64), e(3)]
+        self.x = torch.randn((self.T, 4 * H, D), generator=g).to(torch.bfloat16).to(dev)
+        self.o = torch.empty((self.T, 2 * H, D), dtype=torch.bfloat16, device=dev)
+        self.work = e(qv.qv_run_attention_workspace_size(self.T, 3, run, 2 * H, H, D, 640), torch.uint8)
+
+    def __call__(self, stream=None):
+        qv, (starts, seq, index, slots, status) = self.qv, self.out
+        qv.qv_page_tables(self.runs, self.lens, self.free, self.count, 16, self.table, starts, self.lens, self.count, seq, index,
+                          slots, status, stream=stream)
+        qv.qv_kv_append(self.cache, self.table, seq, index, self.x[:, 4:6], self.x[:, 6:], stream=stream)
+        qv.qv_run_attention(self.x[:, :4], starts, self.run, self.cache, self.table, self.lens, self.o, self.work, window=150,
+                            sinks=4, stream=stream)
+        return self.o
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("run", [6, 100])
+def test_served_in_a_graph_and_on_a_stream(qv, dev, kind, run):
+    """The three calls captured and replayed, with other calls in between that use the workspace, and on a stream of their own,
+    against the eager calls."""
+    eager, graphed, aside = (Serve(qv, dev, kind, run) for _ in range(3))
+    first = eager().clone()
+    graphed.work, graphed.out = eager.work, eager.out  # shared by the two
+    assert torch.equal(graphed(), first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    aside(stream)
+    stream.synchronize()
+    assert torch.equal(aside.o, first)
+    for _ in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        got = graphed.o.clone()
+        assert torch.equal(got, eager()), "replay"
+        aside(stream)
+        stream.synchronize()
+        assert torch.equal(aside.o, got)
+        assert eager.lens.tolist() == graphed.lens.tolist() == aside.lens.tolist()
+        eager.work.fill_(0xFF)  # nothing in the workspace is kept
+        for a, b in ((eager, graphed), (eager, aside)):
+            assert torch.equal(a.table, b.table) and int(a.count) == int(b.count)
+    assert eager.lens.tolist() == [5 * run, 0, 15] and eager.out[4].tolist() == [0, 0, 0]
+    expect = runs64(eager.x[:, :4].cpu(), [0, run, run, run + 3], eager.cache, eager.table.cpu(), eager.lens.tolist(), 150, 4, True, 0.125)
+    check(eager.o, expect, "bf16", rounds(run, 2, "bf16", kind))
+
+
+def test_results_repeat(qv, dev):
+    """Split runs give the same bits on every call."""
+    g = gen(9)
+    lens = [6000, 40]
+    table, pages = shuffled_table(lens, 64, g)
+    cache = make(qv, dev, pages, 2, 64, 128, "bf16", 1)
+    Q = torch.randn((190, 4, 128), generator=g).to(torch.bfloat16).to(dev)
+    first = attend(qv, dev, Q, [0, 150, 190], 150, cache, table, lens)
+    for _ in range(3):
+        assert torch.equal(first, attend(qv, dev, Q, [0, 150, 190], 150, cache, table, lens))
+
+
+@pytest.mark.parametrize("run", [3, 120])
+def test_pages_that_stand_twice(qv, dev, run):
+    """A page that several entries name, and sequences that share their first pages."""
+    g = gen(run)
+    n = 16 * 20 + run
+    entries = -(-n // 16)
+    table = torch.randint(0, 5, (2, entries), generator=g, dtype=torch.int32)
+    table[1, :10] = table[0, :10]
+    cache = make(qv, dev, 5, 2, 16, 64, "bf16", 2)
+    Q = torch.randn((2 * run, 2, 64), generator=g).to(torch.bfloat16)
+    O = attend(qv, dev, Q.to(dev), [0, run, 2 * run], run, cache, table, [n, n])
+    check(O, runs64(Q, [0, run, 2 * run], cache, table, [n, n], 0, 0, True, 0.125), "bf16", rounds(run, 1, "bf16"))
+
+
+def test_many_sequences(qv, dev):
+    """More sequences than a wave has lanes: few rows of each, and long runs with empty ones between."""
+    g = gen(12)
+    for longest in (4, 60):
+        runs = [int(n) if i % 3 else 0 for i, n in enumerate(torch.randint(0, longest + 1, (200,), generator=g))]
+        runs[17] = longest
+        lens = [n + int(m) for n, m in zip(runs, torch.randint(0, 60, (200,), generator=g))]
+        table, pages = shuffled_table(lens, 16, g)
+        cache = make(qv, dev, pages, 1, 16, 64, "int8", 2)
+        Q = torch.randn((sum(runs), 2, 64), generator=g).to(torch.bfloat16)
+        starts = sums(runs)
+        O = attend(qv, dev, Q.to(dev), starts, longest, cache, table, lens, 30, 1)
+        check(O, runs64(Q, starts, cache, table, lens, 30, 1, True, 0.125), "bf16", rounds(longest, 2, "bf16", "int8"))

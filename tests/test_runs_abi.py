@@ -106,6 +106,7 @@ def test_attention_refusals(L):
     assert attend(L, O=heads(ts=0)) == SHAPE and attend(L, O=heads(ts=64, hs=64)) == SHAPE   # rows that share memory
     assert attend(L, work=None) == WORKSPACE and attend(L, work=P + 64) == ALIGN
     assert attend(L, pages=1 << 27, ld=1 << 27) == UNSUPPORTED                # 2^32 places
+    assert attend(L, pages=(1 << 26) - 1, ld=1 << 26) == UNSUPPORTED          # 2^31 - 32: the last step passes 2^31
     assert attend(L, T=1 << 31, B=1 << 31, max_run=1) == UNSUPPORTED
     assert attend(L, T=1 << 30, B=1 << 30, max_run=1) == UNSUPPORTED
     assert attend(L, T=1 << 28, max_run=1 << 28) == UNSUPPORTED               # rows of a join
