@@ -1,5 +1,10 @@
 // run_attention.hip -- attention of short runs of tokens (and of single ones that keep first tokens in sight) over a paged
 // cache: the kernels of paged_attention.h with the rows of a run in the place of a token's query heads.
+//
+// Bound by memory where a run has up to 16 rows to a cache head: one token of each of 32 sequences with a window of 4096 and four
+// first tokens (513 MB) takes 108 + 5 us, 4.5 TB/s.  More rows go in tiles of 16, each of which reads and converts the tokens again: 16
+// runs of 5 tokens of 4 query heads over up to 8192 in int8 (62 MB) 26 + 5 us.  Their blocks follow each other on one die,
+// whose cache then has what the first one read: bf16 38 us instead of 49, int8 32 instead of 35.
 #include "paged_attention.h"
 #include "qv_runs_internal.h"
 

@@ -8,15 +8,27 @@
 //                   sum need one exchange between the halves of a wave.
 //   O^T += V^T P^T  a lane's own probabilities are its operand: slot 8 h + j of 16 tokens (h = lane / 32) stands for token
 //                   4 h + j (j < 4) or 4 h + j + 4, on both sides.  V is read from LDS transposed.
-// Both are v_mfma_f32_32x32x16_bf16; queries stay in registers, keys and values go global -> registers -> LDS while the tile
-// before is worked on (two buffers, one barrier a tile); 8-bit caches are converted on the way, once for the four waves.
-// In LDS a 16-byte piece of a row lies at its number xor the row's: reads of one piece of eight rows, and transposed reads of
-// 32 channels of four rows, then fall on different banks.
+// Both are v_mfma_f32_32x32x16_bf16; queries stay in registers, and keys and values of the next step are on their way while one
+// is worked on (two buffers, one barrier a step): bf16 straight to LDS, 8-bit codes by way of registers, converted once for the four
+// waves.  In LDS a 16-byte piece of a token lies at its number xor some bits of the token's (key_xor, value_xor).
 //
-// bf16 queries: probabilities are rounded to bf16 for the second product (to nearest, 2^-9 of each on average and of either
-// sign, as much as the result's own rounding); their sum is of the unrounded ones.  fp32 queries and their probabilities
-// are three bf16 pieces that sum to them.
+// bf16 queries: probabilities are rounded to bf16 for the second product (to nearest, 2^-8 of each at most and of either sign, as the
+// result's own rounding is); their sum is of the unrounded ones.  Two pieces that sum to them would take half as many matrix
+// instructions again.  fp32 queries and their probabilities are three bf16 pieces that sum to them.
 // The maximum that scales a row's probabilities is raised only when one passes 2^8 of it: sums are fp32, and the rest follows.
+//
+// Bound by the matrix cores and the vector ALU (32 exponentials, 32 multiply-adds and 32 sums of a lane to 32 matrix instructions of
+// 128 channels) together: four prompts of up to 8192 tokens (8 heads of 128, 32 queries, causal) take 0.96 to 1.0 ms, 1.0 to 1.06
+// PFLOP/s where a library product of 8192^3 reaches 1.22; the matrix cores are busy for 50 % of the time, the vector ALU for 49 %.
+// A frame of 1374 tokens over eight (16 heads of 64) takes 97 us, 640 TFLOP/s: with 64 channels the vector ALU has twice as
+// much to do for a matrix instruction (50 and 30 % busy).  A chunk of up to 611 tokens over 4001 of the FP8 cache 90 us (conversions,
+// join), fp32 prompts of up to 1833 tokens with a window of 1000 in 42 us (one wave a SIMD, 1100 waves of a dozen steps).
+//
+// Tried (us: frame over eight, prompts of 8192): staging bf16 by way of registers and masks in every step 179, 1505; steps whose
+// way depends on masks only through a branch that changes scores 133, 1089; scalar addresses for the loads to LDS 140, 962 where it was
+// 138, 1029; scores formed a step ahead, behind the product of the step before, 114, 1036 where it was 103, 984; matrix and vector
+// instructions dealt out in turn by the scheduler 145, 1097 where it was 140, 1061; eight waves and 256 rows to a block 119, 988 where
+// it was 100, 977; four waves a SIMD for 64 channels (registers spill) 123 where it was 103.
 #include <type_traits>
 
 #include "paged_attention.h"
