@@ -1,7 +1,8 @@
 """Frames enter a block's paged cache, then single tokens are answered from it: the few-row 4-bit linears, the append
-with the position rotation and the paged attention in one captured step.
+with the position rotation and the paged attention in one captured step.  With --attend the frames' tokens attend to each other and
+to the frames before, and the sequences share their pages.
 
-    python examples/stream_block.py [--frames 2] [--sequences 4] [--tokens 64] [--int8]
+    python examples/stream_block.py [--frames 2] [--sequences 4] [--tokens 64] [--int8 | --fp8] [--attend] [--window 4096] [--sinks 5]
 """
 import argparse
 import os
@@ -32,16 +33,28 @@ def main(argv=None):
     ap.add_argument("--sequences", type=int, default=4)
     ap.add_argument("--tokens", type=int, default=64)
     ap.add_argument("--int8", action="store_true", help="int8 cache instead of bf16")
+    ap.add_argument("--fp8", action="store_true", help="cache of 8-bit floating-point codes instead of bf16")
+    ap.add_argument("--attend", action="store_true", help="frames are answered as well")
+    ap.add_argument("--window", type=int, default=0, help="tokens that one looks back on (0: all)")
+    ap.add_argument("--sinks", type=int, default=0, help="first tokens that stay visible")
     a = ap.parse_args(argv)
     dev = torch.device("cuda:0")
     T = synth.FRAME_TOKENS
     weights = {lin.name: synth.weights_torch(lin.N, lin.K, lin.w_seed, dev) for lin in configs.block_linears()}
-    block = StreamBlock(qv, weights, a.sequences, a.frames * T + a.tokens + 8, dev, axes=2, positions=GRID + 1, base=100.0,
-                        int8_cache=a.int8, frame_tokens=T)
+    room = a.frames * T + a.tokens + 8
+    block = StreamBlock(qv, weights, a.sequences, room, dev, axes=2, positions=GRID + 1, base=100.0, int8_cache=a.int8,
+                        frame_tokens=T * (a.sequences if a.attend else 1), fp8_cache=a.fp8, window=a.window, sinks=a.sinks,
+                        pages=a.sequences * -(-room // 64) if a.attend else None)
     where = frame_positions(dev)
-    for s in range(a.sequences):
-        for f in range(a.frames):
-            block.take_frame(synth.vggt_activations_torch(T, 1024, 1000 * s + f, torch.bfloat16, dev), s, where)
+    frame = lambda s, f: synth.vggt_activations_torch(T, 1024, 1000 * s + f, torch.bfloat16, dev)
+    for f in range(a.frames):
+        if a.attend:  # a frame of every sequence at once
+            x = torch.cat([frame(s, f) for s in range(a.sequences)])
+            y = block.take_runs(x, [T] * a.sequences, where.repeat(a.sequences, 1), causal=False)
+            assert bool(torch.isfinite(y.float()).all())
+        else:
+            for s in range(a.sequences):
+                block.take_frame(frame(s, f), s, where)
     x = torch.randn((a.sequences, 1024), device=dev).to(torch.bfloat16)
     out = block.step(x)  # once eagerly, then captured
     graph = torch.cuda.CUDAGraph()
@@ -55,7 +68,7 @@ def main(argv=None):
     torch.cuda.synchronize()
     us = (time.perf_counter() - t) / a.tokens * 1e6
     assert bool(torch.isfinite(out.float()).all())
-    print(f"{a.sequences} sequences of {a.frames} frames, {'int8' if a.int8 else 'bf16'} cache: "
+    print(f"{a.sequences} sequences of {a.frames} frames, {'int8' if a.int8 else 'fp8' if a.fp8 else 'bf16'} cache: "
           f"{us:.1f} us a step, lengths {block.lens.tolist()}")
     return block, out
 

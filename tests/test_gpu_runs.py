@@ -751,3 +751,56 @@ def test_many_sequences(qv, dev):
         starts = sums(runs)
         O = attend(qv, dev, Q.to(dev), starts, longest, cache, table, lens, 30, 1)
         check(O, runs64(Q, starts, cache, table, lens, 30, 1, True, 0.125), "bf16", rounds(longest, 2, "bf16", "int8"))
+
+
+@pytest.mark.parametrize("share", [1, 3])
+def test_runs_of_one_or_none(qv, dev, share):
+    """Single tokens of some sequences, with and without tokens before them."""
+    g = gen(share)
+    runs, before = [1, 0, 1, 0, 1, 1], [0, 40, 700, 0, 15, 16]
+    lens = [n + m for n, m in zip(runs, before)]
+    table, pages = shuffled_table(lens, 16, g)
+    for kind in ("bf16", "fp8"):
+        cache = make(qv, dev, pages, 2, 16, 64, kind, 3)
+        Q = torch.randn((5, 2 * share, 64), generator=g).to(torch.bfloat16)
+        starts = sums(runs)
+        for window, sinks in ((0, 0), (30, 2)):
+            O = attend(qv, dev, Q.to(dev), starts, 1, cache, table, lens, window, sinks)
+            check(O, runs64(Q, starts, cache, table, lens, window, sinks, True, 0.125), "bf16", False)
+            assert bool(torch.isnan(O[4:].float()).all())
+
+
+@pytest.mark.parametrize("run", [7, 150])
+@pytest.mark.parametrize("window,sinks,causal", [(1, 0, True), (1, 1, True), (2, 0, False), (64, 64, True), (1 << 40, 3, True), (5, 1 << 40, True)])
+def test_narrow_and_wide_windows(qv, dev, run, window, sinks, causal):
+    g = gen(run)
+    lens = [run + 77, run]
+    table, pages = shuffled_table(lens, 16, g)
+    cache = make(qv, dev, pages, 2, 16, 64, "bf16", 3)
+    Q = torch.randn((2 * run, 2, 64), generator=g).to(torch.bfloat16)
+    starts = sums([run] * 2)
+    O = attend(qv, dev, Q.to(dev), starts, run, cache, table, lens, window, sinks, causal)
+    check(O, runs64(Q, starts, cache, table, lens, window, sinks, causal, 0.125), "bf16", rounds(run, 1, "bf16"))
+    if window == 1 and sinks == 0:  # a token sees itself alone
+        t = torch.arange(lens[0] - run, lens[0])
+        v = cache.v_pages.cpu()[table[0].long()[t // 16], :, t % 16]
+        assert torch.equal(O[:run].cpu(), v)
+
+
+def test_queries_that_are_not_numbers(qv, dev):
+    """A query of NaN or infinity gives NaN in its row and nowhere else."""
+    g = gen(4)
+    for run, kind in ((9, "bf16"), (140, "bf16"), (140, "int8")):
+        lens = [run + 50]
+        table, pages = shuffled_table(lens, 16, g)
+        cache = make(qv, dev, pages, 2, 16, 64, kind, 3)
+        Q = torch.randn((run, 4, 64), generator=g).to(torch.bfloat16)
+        clean = runs64(Q, [0, run], cache, table, lens, 0, 0, True, 0.125)
+        Q[3, 1, 5], Q[run - 2, 2] = float("nan"), float("inf")
+        O = attend(qv, dev, Q.to(dev), [0, run], run, cache, table, lens).cpu()
+        for row, head in ((3, 1), (run - 2, 2)):
+            assert bool(torch.isnan(O[row, head]).all())
+            for x in clean:
+                x[row, head] = float("nan")
+            O[row, head] = 0
+        check(O, clean, "bf16", rounds(run, 2, "bf16", kind))

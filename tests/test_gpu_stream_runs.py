@@ -119,3 +119,17 @@ def test_pages_come_back(qv, dev, weights):
         block.take_runs(rows(65, g, dev), [65, 0, 0], places(65, g, dev))
     with pytest.raises(ValueError, match="int8 or FP8"):
         make(qv, dev, weights, int8_cache=True, fp8_cache=True)
+
+
+@pytest.mark.parametrize("flags", [["--attend"], ["--fp8", "--attend", "--window", "1500", "--sinks", "5"], ["--fp8"]])
+def test_example(dev, flags):
+    import sys
+
+    from test_decode_abi import ROOT
+
+    sys.path.insert(0, ROOT + "/examples")
+    import stream_block
+
+    block, out = stream_block.main(["--frames", "2", "--sequences", "2", "--tokens", "6", *flags])
+    # one eager step and six replays behind two frames
+    assert block.lens.tolist() == [2 * 1374 + 7] * 2 == block.held and bool(torch.isfinite(out.float()).all())
