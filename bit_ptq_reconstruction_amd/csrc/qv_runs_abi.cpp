@@ -21,7 +21,9 @@ bool run_sizes(int64_t T, int64_t B, int64_t max_run, int64_t q_heads, int64_t h
     if (T > kMaxInt / q_heads / 32 || t.items * t.parts > kMaxThreads / 256 / heads) return false;
   }
   if (qv::long_runs(max_run, q_heads, heads, true)) return true;
-  return attention_fits(B, q_heads * max_run, qv::paged_attention_parts(B, q_heads * max_run, heads, capacity));
+  qv::AttentionParts p = qv::paged_attention_parts(B, q_heads * max_run, heads, capacity);
+  p.most += 8;  // the blocks of a tile of rows are rounded up to eight
+  return attention_fits(B, q_heads * max_run, p);
 }
 
 }  // namespace

@@ -501,6 +501,15 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
       }
       if (n16 < 3) probabilities((n16 + 1) >> 1, (n16 + 1) & 1, p[(n16 + 1) & 1]);
     }
+    // fp32 queries of 128 channels leave room for one wave a SIMD: its vector instructions go between its own matrix instructions (two
+    // prompts of up to 4000 tokens 0.60 ms where it was 0.63; with two waves a SIMD there is nothing to gain).
+    if constexpr (NP == 3 && D == 128 && KIND == kBf16 && !CAREFUL) {
+#pragma unroll
+      for (int i = 0; i < 3 * NP * kC; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x402, 72 / (NP * kC), 0);
+      }
+    }
     if constexpr (KIND == kBf16) __builtin_amdgcn_s_setprio(0);
     if constexpr (CAREFUL) {
       const u32x4* const mine = &vs[buffer][lane * kRowPieces];  // lane i looks at token i
