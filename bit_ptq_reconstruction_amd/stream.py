@@ -25,7 +25,8 @@ class StreamBlock:
 
     The cache for ``sequences`` sequences of up to ``capacity`` tokens (rounded up to whole pages), the workspaces and the
     linears' and the attention's outputs are allocated here, so a step can be captured in a graph.  The norms and residual
-    sums are torch's and allocate theirs (under capture from the graph's pool), and so does take_frame().
+    sums are torch's and allocate theirs (under capture from the graph's pool), and so do take_frame()
+    and take_runs(), which reads its runs on the host and is not for capture.
 
     ``positions`` places along each of ``axes`` axes have an angle; the output of a token at another one, and of those that
     come after it in its sequence, is NaN.  A frame, or the runs of one call, has up to ``frame_tokens`` tokens."""

@@ -77,3 +77,11 @@ def test_fp8_cache():
 
 def test_names():
     assert qv.QV_KV_FP8 == 2 and [qv.QV_RUN_OK, qv.QV_RUN_NO_ROOM, qv.QV_RUN_NO_PAGES, qv.QV_RUN_NO_ROWS] == [0, 1, 2, 3]
+
+
+def test_stream_block_of_two_caches():
+    """Refused before anything is allocated."""
+    from bit_ptq_reconstruction_amd.stream import StreamBlock
+
+    with pytest.raises(ValueError, match="int8 or FP8"):
+        StreamBlock(None, {}, 1, 16, "cpu", int8_cache=True, fp8_cache=True)
