@@ -220,6 +220,8 @@ class StreamBlock:
         qv.qv_run_attention(b["q"], starts, max(runs), self.cache, self.table, self.lens, b["o"], parts, window=self.window,
                             sinks=self.sinks, causal=causal)
         y = x + self._linear("proj", b["o"].view(T, self.width), b, few=False)
+        # The linears' rounding to 4 bits takes finite rows.  A token that was not stored makes every channel of every head NaN.
+        y.masked_fill_(b["o"][:, 0, :1].isnan(), float("nan"))
         return y + self._linear("fc2", self._linear("fc1", self._norm(y), b, few=False), b, few=False)
 
     def step(self, x):

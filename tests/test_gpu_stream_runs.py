@@ -133,3 +133,22 @@ def test_example(dev, flags):
     block, out = stream_block.main(["--frames", "2", "--sequences", "2", "--tokens", "6", *flags])
     # one eager step and six replays behind two frames
     assert block.lens.tolist() == [2 * 1374 + 7] * 2 == block.held and bool(torch.isfinite(out.float()).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "int8", "fp8"])
+def test_position_outside_in_a_run(qv, dev, weights, cache):
+    """A token at a place without an angle: its output and those behind it in its sequence are NaN, those before it and the other
+    sequence's are what they are without it."""
+    g = gen(9)
+    x, at = rows(50, g, dev), places(50, g, dev)
+    outs = []
+    for bad in (False, True):
+        block = make(qv, dev, weights, sequences=2, capacity=48, frame_tokens=50, int8_cache=cache == "int8", fp8_cache=cache == "fp8")
+        if bad:
+            at[20, 0] = 40
+        outs.append(block.take_runs(x, [35, 15], at).float())
+    clean, spoilt = outs
+    assert bool(torch.isnan(spoilt[20:35]).all()) and bool(torch.isfinite(clean).all())
+    if cache != "fp8":  # where the other tokens of the page share its scale
+        assert torch.equal(spoilt[:20], clean[:20])
+    assert torch.equal(spoilt[35:], clean[35:]) and bool(torch.isfinite(spoilt[:20]).all())
