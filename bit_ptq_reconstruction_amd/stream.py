@@ -141,9 +141,16 @@ class StreamBlock:
         return starts, seq[:rows], index[:rows]
 
     def end(self, sequence: int) -> None:
-        """The sequence is over: it has no tokens, and its pages are free again where they are shared."""
+        """The sequence is over: it has no tokens, its pages hold NaN as at the start and are free again where they are shared."""
+        import torch
+
+        n = self._pages(self.held[sequence])
+        pages = self.table[sequence, :n].long()
+        for content, scales in ((self.cache.k_pages, self.cache.k_scale), (self.cache.v_pages, self.cache.v_scale)):
+            if content.dtype == torch.float8_e4m3fn:
+                content.view(torch.uint8)[pages] = 0x7F  # NaN
+            (content if scales is None else scales)[pages] = float("nan")
         if self.pooled:
-            n = self._pages(self.held[sequence])
             self.free[self.left:self.left + n] = self.table[sequence, :n]
             self.table[sequence, :n] = -1
             self.left += n

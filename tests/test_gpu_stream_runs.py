@@ -152,3 +152,24 @@ def test_position_outside_in_a_run(qv, dev, weights, cache):
     if cache != "fp8":  # where the other tokens of the page share its scale
         assert torch.equal(spoilt[:20], clean[:20])
     assert torch.equal(spoilt[35:], clean[35:]) and bool(torch.isfinite(spoilt[:20]).all())
+
+
+@pytest.mark.parametrize("pages", [None, 6])
+@pytest.mark.parametrize("cache", ["bf16", "int8", "fp8"])
+def test_position_outside_on_pages_used_before(qv, dev, weights, cache, pages):
+    """A token at a place without an angle is not stored: it and those behind it in its sequence are NaN, whatever sequence had the
+    pages before; those before it and the other sequence are not."""
+    block = make(qv, dev, weights, sequences=2, capacity=48, frame_tokens=60, int8_cache=cache == "int8", fp8_cache=cache == "fp8",
+                 pages=pages)
+    g = gen(8)
+    block.take_runs(rows(60, g, dev), [40, 20], places(60, g, dev))
+    for s in range(2):
+        block.end(s)
+    at = places(50, g, dev)
+    at[20] = torch.tensor([40, 3])
+    out = block.take_runs(rows(50, g, dev), [35, 15], at).float()
+    assert bool(torch.isnan(out[20:35]).all()) and bool(torch.isfinite(out[:20]).all()) and bool(torch.isfinite(out[35:]).all())
+    block.position.zero_()
+    out = block.step(rows(2, g, dev)).float()
+    assert bool(torch.isnan(out[0]).all()) and bool(torch.isfinite(out[1]).all())
+    assert block.lens.tolist() == block.held == [36, 16]
