@@ -12,19 +12,21 @@
 // is worked on (two buffers, one barrier a step): bf16 straight to LDS, 8-bit codes by way of registers, converted once for the four
 // waves.  In LDS a 16-byte piece of a token lies at its number xor some bits of the token's (key_xor, value_xor).
 //
-// bf16 queries: probabilities are rounded to bf16 for the second product (to nearest, 2^-8 of each at most and of either sign, as the
-// result's own rounding is); their sum is of the unrounded ones.  Two pieces that sum to them would take half as many matrix
-// instructions again.  fp32 queries and their probabilities are three bf16 pieces that sum to them.
+// bf16 queries: a probability is two bf16 pieces for the second product, each to the nearest, which leave 2^-17 of it at most and of
+// either sign, of the order of its score's fp32 rounding; their sum is of the whole ones.  One piece, with two thirds of
+// the matrix instructions, leaves 2^-8 and a result that is 2.1 to 2.3e-3 off in the 2-norm where its own rounding makes 1.6 to
+// 1.7e-3 (us with one piece and with two: frame over eight 89 and 116, chunk in FP8 91 and 102, prompts of up to 8192 982 and 1369).
+// fp32 queries and their probabilities are three bf16 pieces that sum to them.
 // The maximum that scales a row's probabilities is raised only when one passes 2^8 of it: sums are fp32, and the rest follows.
 //
 // Bound by the matrix cores and the vector ALU (32 exponentials, 32 multiply-adds and 32 sums of a lane to 32 matrix instructions of
-// 128 channels) together: four prompts of up to 8192 tokens (8 heads of 128, 32 queries, causal) take 0.96 to 1.0 ms, 1.0 to 1.06
-// PFLOP/s where a library product of 8192^3 reaches 1.22; the matrix cores are busy for 50 % of the time, the vector ALU for 49 %.
-// A frame of 1374 tokens over eight (16 heads of 64) takes 97 us, 640 TFLOP/s: with 64 channels the vector ALU has twice as
-// much to do for a matrix instruction (50 and 30 % busy).  A chunk of up to 611 tokens over 4001 of the FP8 cache 90 us (conversions,
+// 128 channels) together: four prompts of up to 8192 tokens (8 heads of 128, 32 queries, causal) take 1.37 ms, 0.73
+// PFLOP/s, where a library product of 8192^3 reaches 1.22: the second product's two pieces make it half as many matrix instructions
+// again (1.10 PFLOP/s).  A frame of 1374 tokens over eight (16 heads of 64) takes 116 us, 535 TFLOP/s: with 64 channels the vector ALU
+// has twice as much to do for a matrix instruction.  A chunk of up to 611 tokens over 4001 of the FP8 cache 102 us (conversions,
 // join), fp32 prompts of up to 1833 tokens with a window of 1000 in 42 us (one wave a SIMD, 1100 waves of a dozen steps).
 //
-// Tried (us: frame over eight, prompts of 8192): staging bf16 by way of registers and masks in every step 179, 1505; steps whose
+// Tried with one piece to a probability (us: frame over eight, prompts of 8192): staging bf16 by way of registers and masks in every step 179, 1505; steps whose
 // way depends on masks only through a branch that changes scores 133, 1089; scalar addresses for the loads to LDS 140, 962 where it was
 // 138, 1029; scores formed a step ahead, behind the product of the step before, 114, 1036 where it was 103, 984; matrix and vector
 // instructions dealt out in turn by the scheduler 145, 1097 where it was 140, 1061; eight waves and 256 rows to a block 119, 988 where
@@ -122,6 +124,14 @@ __device__ __forceinline__ unsigned cut(float& x, float& y) {
   return w;
 }
 
+// The nearest bf16 pieces of two numbers, which leave the numbers.
+__device__ __forceinline__ unsigned cut_nearest(float& x, float& y) {
+  const unsigned w = pack(x, y);
+  x -= bits_float(w << 16);
+  y -= bits_float(w & 0xFFFF0000u);
+  return w;
+}
+
 __device__ __forceinline__ bool odd_pair(unsigned w) {  // an infinity or NaN among two bf16 values
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
@@ -161,7 +171,8 @@ __device__ __forceinline__ void arrive() {
 template <int D, typename X, int KIND>
 __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void tiles_kernel(TileArgs t) {
   const Args& a = t.a;
-  constexpr int NP = sizeof(X) == 2 ? 1 : 3;      // bf16 pieces of a query and of a probability
+  constexpr int NQ = sizeof(X) == 2 ? 1 : 3;      // bf16 pieces of a query
+  constexpr int NP = sizeof(X) == 2 ? 2 : 3;      // of a probability
   constexpr int kElem = KIND == kBf16 ? 2 : 1;
   constexpr int kPieces = D * kElem / 16;         // 16-byte loads of a token
   constexpr int kPass = kN * kPieces / kThreads;  // loads of a thread
@@ -202,13 +213,13 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   const bool live = row0 < rows;
 
   const float scale = fabsf(a.scale);
-  bf16x8 q[kK][NP];
+  bf16x8 q[kK][NQ];
   {
     const X* const x = static_cast<const X*>(a.q) + (int64_t)(item.run.s0 + token) * a.q_ts + (int64_t)head * a.q_hs + 8 * half;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
       float v[8];
-      if constexpr (NP == 1) {
+      if constexpr (NQ == 1) {
         const u32x4 w = *reinterpret_cast<const u32x4*>(x + 16 * k);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = bits_float(w[i] << 16), v[2 * i + 1] = bits_float(w[i] & 0xFFFF0000u);
@@ -222,7 +233,7 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
         for (int i = 0; i < 8; ++i) v[i] *= a.scale < 0.0f ? -1.0f : 0.0f;
       }
 #pragma unroll
-      for (int n = 0; n < NP; ++n) {
+      for (int n = 0; n < NQ; ++n) {
         u32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = cut(v[2 * i], v[2 * i + 1]);
@@ -366,7 +377,7 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
     const u32x4* const kt = &ks[0][0] + buffer * kBuffer;
     f32x16 acc[2] = {f32x16{}, f32x16{}};
     // Keys are read a group of operands ahead of the products.
-    constexpr int kGroup = D == 64 && NP == 1 ? 4 : 2;
+    constexpr int kGroup = D == 64 && NQ == 1 ? 4 : 2;
     bf16x8 f[2][kGroup][2];
     auto read_keys = [&](int group) {
 #pragma unroll
@@ -387,7 +398,7 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int n = NP - 1; n >= 0; --n)
+          for (int n = NQ - 1; n >= 0; --n)
             acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[group & 1][k][u], q[group * kGroup + k][n], acc[u], 0, 0, 0);
     }
     if constexpr (KIND == kBf16) __builtin_amdgcn_s_setprio(0);
@@ -458,7 +469,8 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
       for (int n = 0; n < NP; ++n) {
         u32x4 w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = NP == 1 ? pack(x[2 * i], x[2 * i + 1]) : cut(x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 4; ++i)
+          w[i] = NP == 3 ? cut(x[2 * i], x[2 * i + 1]) : (n == 0 ? cut_nearest(x[2 * i], x[2 * i + 1]) : pack(x[2 * i], x[2 * i + 1]));
         p[n] = __builtin_bit_cast(bf16x8, w);
       }
     };
@@ -587,7 +599,7 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = l == 0.0f ? 0.0f : o[d][4 * g + i] * inverse;
-        if constexpr (NP == 1)
+        if constexpr (sizeof(X) == 2)
           *reinterpret_cast<u32x2*>(to + 32 * d + 8 * g) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
         else
           *reinterpret_cast<f32x4*>(to + 32 * d + 8 * g) = f32x4{v[0], v[1], v[2], v[3]};

@@ -72,10 +72,10 @@ size_t qv_run_attention_workspace_size(int64_t T, int64_t B, int64_t max_run, in
  *   scale       finite;  window >= 0, sinks >= 0.
  *   O           [T][q_heads][head_dim] of Q's type.  A row that sees no token gives zeros; a query of NaN, or a NaN among the
  *               tokens that a row sees, gives NaN; what a row does not see does not count, whatever it holds.
- *               Scores, softmax and sums are fp32.  bf16 queries in runs with more than QV_RUN_FEW_ROWS rows to a cache head
- *               (QV_RUN_FEW_ROWS_8BIT over 8-bit caches), max_run * q_heads / heads, have their probabilities rounded to bf16
- *               for the product with the values; else they are not rounded.  An fp32 query is taken as three bf16 pieces
- *               that sum to it.
+ *               Scores, softmax and sums are fp32.  For the product with the values, bf16 queries in runs with more than
+ *               QV_RUN_FEW_ROWS rows to a cache head (QV_RUN_FEW_ROWS_8BIT over 8-bit caches), max_run * q_heads / heads, have
+ *               each probability as two bf16 pieces that leave 2^-17 of it at most; else it is not rounded.  An fp32 query is
+ *               taken as three bf16 pieces that sum to it.
  *   workspace   at least qv_run_attention_workspace_size bytes, 256-byte aligned, reused freely.
  */
 #define QV_RUN_FEW_ROWS 32
