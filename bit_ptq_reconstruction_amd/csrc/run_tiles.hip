@@ -23,7 +23,7 @@
 // 128 channels) together: four prompts of up to 8192 tokens (8 heads of 128, 32 queries, causal) take 1.37 ms, 0.73
 // PFLOP/s, where a library product of 8192^3 reaches 1.22: the second product's two pieces make it half as many matrix instructions
 // again (1.10 PFLOP/s).  A frame of 1374 tokens over eight (16 heads of 64) takes 116 us, 535 TFLOP/s: with 64 channels the vector ALU
-// has twice as much to do for a matrix instruction.  A chunk of up to 611 tokens over 4001 of the FP8 cache 102 us (conversions,
+// has twice as much to do for a matrix instruction.  A chunk of up to 611 tokens over 4001 of the FP8 cache 99 us (conversions,
 // join), fp32 prompts of up to 1833 tokens with a window of 1000 in 42 us (one wave a SIMD, 1100 waves of a dozen steps).
 //
 // Tried with one piece to a probability (us: frame over eight, prompts of 8192): staging bf16 by way of registers and masks in every step 179, 1505; steps whose
@@ -159,9 +159,6 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t lane_byte
 __device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
 }
-// Loads above stay in their branch.  (Merged with those of another branch, the compiler gave them an address that one way there
-// left undefined.)
-__device__ __forceinline__ void keep_apart() { asm volatile("" ::: "memory"); }
 // All loads to LDS of the block have landed, and all waves are here.
 __device__ __forceinline__ void arrive() {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -267,14 +264,13 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
   // whole step, lanes of tokens that none sees read the nearest one that is seen (or anything, if that has no page).
   constexpr int kBuffer = kN * kRowPieces;  // pieces of a buffer
   constexpr int kHeld = KIND == kBf16 ? 1 : kPass;
-  u32x4 kr[kHeld], vr[kHeld];
+  u32x4 kr[kHeld] = {}, vr[kHeld] = {};
   float scale_r = 0.0f;
   const int my_token = threadIdx.x / kPieces, my_piece = threadIdx.x % kPieces;
   const uint32_t token_bytes = a.token_stride * kElem;
   const int kx_write = key_xor<D>(my_token), vx_write = value_xor<D>(my_token);
-  // The lane's piece in a token; bf16: the one whose place in LDS is the lane's.
-  const uint32_t k_piece = 16 * (KIND == kBf16 ? my_piece ^ kx_write : my_piece);
-  const uint32_t v_piece = 16 * (KIND == kBf16 ? my_piece ^ vx_write : my_piece);
+  // bf16: the lane's piece in a token is the one whose place in LDS is the lane's.
+  const uint32_t k_piece = 16 * (my_piece ^ kx_write), v_piece = 16 * (my_piece ^ vx_write);
   const uint32_t k_bytes = (my_token % 16) * token_bytes + k_piece, v_bytes = (my_token % 16) * token_bytes + v_piece;
   // Where a wave's pieces of the first buffer go, and the values behind the keys.
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&ks[0][0] + 1024 * wave);
@@ -284,42 +280,38 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
     if (number % 16 == 0) look_up(step);
     const int t0 = steps.first_token(step);
     const unsigned paged = __ballot(at >= 0) >> lane0 & 15;
-    if (paged == 0) {
-      keep_apart();
-      return paged;
-    }
+    if (paged == 0) return paged;
     const bool whole = paged == 15 && t0 >= steps.all_low && t0 + kN <= steps.all_high;
     const uint32_t to = lds0 + (number & 1) * (16 * kBuffer);
-    if (whole) {
+    auto nearest = [&](int i) {  // where the i-th token of the thread, or the nearest one that is seen, begins
+      int tk = t0 + i * kTokens + my_token;
+      tk = tk < steps.high ? tk : steps.high - 1;
+      if (tk < steps.low && tk >= steps.sinks) tk = steps.sinks > t0 ? steps.sinks - 1 : steps.low;
+      const int64_t group = __shfl(at, lane0 + ((tk - t0) >> 4));
+      return (group < 0 ? 0 : group) + (int64_t)((uint64_t)(tk & 15) * token_bytes);
+    };
+    if constexpr (KIND == kBf16) {
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        const int64_t from = lane_value(at, lane0 + (i * kTokens + wave * (kTokens / 4)) / 16);  // a group is the same in a wave
-        if constexpr (KIND == kBf16) {  // a wave's 64 pieces go side by side
+        if (whole) {  // a group is the same in a wave, whose 64 pieces go side by side
+          const int64_t from = lane_value(at, lane0 + (i * kTokens + wave * (kTokens / 4)) / 16);
           load_to_lds(a.kp + from, k_bytes, to + i * 4096);
           load_to_lds(a.vp + from, v_bytes, to + i * 4096 + values_at);
         } else {
-          kr[i] = *reinterpret_cast<const u32x4*>(a.kp + from + k_bytes);
-          vr[i] = *reinterpret_cast<const u32x4*>(a.vp + from + v_bytes);
-        }
-      }
-      keep_apart();
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPass; ++i) {
-        int tk = t0 + i * kTokens + my_token;
-        tk = tk < steps.high ? tk : steps.high - 1;
-        if (tk < steps.low && tk >= steps.sinks) tk = steps.sinks > t0 ? steps.sinks - 1 : steps.low;
-        const int64_t group = __shfl(at, lane0 + ((tk - t0) >> 4));
-        const int64_t from = (group < 0 ? 0 : group) + (uint64_t)(tk & 15) * token_bytes;
-        if constexpr (KIND == kBf16) {
+          const int64_t from = nearest(i);
           load_to_lds(a.kp + from + k_piece, to + i * 4096);
           load_to_lds(a.vp + from + v_piece, to + i * 4096 + values_at);
-        } else {
-          kr[i] = *reinterpret_cast<const u32x4*>(a.kp + from + k_piece);
-          vr[i] = *reinterpret_cast<const u32x4*>(a.vp + from + v_piece);
         }
       }
-      keep_apart();
+    } else {
+      // One load for both, whose address is formed on one way alone.  (Loads on two ways were merged by the compiler, with an
+      // address that was set on one of them.)  Of a whole step every token is its own nearest one.
+#pragma unroll
+      for (int i = 0; i < kPass; ++i) {
+        const int64_t from = nearest(i) + 16 * my_piece;
+        kr[i] = *reinterpret_cast<const u32x4*>(a.kp + from);
+        vr[i] = *reinterpret_cast<const u32x4*>(a.vp + from);
+      }
     }
     if constexpr (KIND != kBf16) {
       if (wave < 2) {  // 64 scales of keys, 64 of values
