@@ -314,9 +314,11 @@ __global__ __launch_bounds__(kThreads, sizeof(X) == 4 && D == 128 ? 1 : 2) void 
       }
     }
     if constexpr (KIND != kBf16) {
-      if (wave < 2) {  // 64 scales of keys, 64 of values
+      if (wave < 2) {  // 64 scales of keys, 64 of values; of tokens that no row sees none, which may be anything
         const int64_t from = __shfl(at, lane0 + lane / 16), s = __shfl(scale_at, lane0 + lane / 16);
-        scale_r = from >= 0 ? (wave == 0 ? a.ks : a.vs)[KIND == kFp8 ? s : s + lane % 16] : 0.0f;
+        const int tk = t0 + lane;
+        const bool seen = tk < steps.high && (tk >= steps.low || tk < steps.sinks);
+        scale_r = seen && from >= 0 ? (wave == 0 ? a.ks : a.vs)[KIND == kFp8 ? s : s + lane % 16] : 0.0f;
       }
     }
     return paged;

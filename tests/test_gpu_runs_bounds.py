@@ -1,4 +1,4 @@
-"""Attention of runs of tokens: what the probabilities' pieces leave of them.
+"""Attention of runs of tokens: what the probabilities' pieces leave of them, and what tokens that no row sees cost.
 
 The probabilities of a bf16 query are two bf16 pieces, each to the nearest: one in [1, 2) leaves at most 2^-8 to the second,
 whose last place is then 2^-16, so that 2^-17 of it is lost at most.  With the rest of test_gpu_runs' bound an element is held to
@@ -34,3 +34,52 @@ def test_probabilities_of_bf16_queries(qv, dev, kind, runs, before, heads, share
     o, mag, _ = runs64(Q, starts, cache, table, lens, window, sinks, causal, dim ** -0.5)
     worst = ((O - o).abs() / ((1e-5 + LOST) * mag + 1.01 * BF * o.abs() + 1e-38)).max().item()
     assert worst <= 1.0, f"{worst:.2f} of the bound"
+
+
+def fastest(call, times=30):
+    """ms of a call among others."""
+    best = float("inf")
+    for _ in range(times):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(4):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) / 4)
+    return best
+
+
+@pytest.mark.parametrize("seqs,before,run,window,causal", [(1, 0, 5502, 0, False), (64, 1003, 128, 900, True)])
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_scales_that_no_row_needs(qv, dev, kind, seqs, before, run, window, causal):
+    """Scales of NaN behind a sequence's end, as a new cache has them, and before its window change neither the result nor the
+    time."""
+    heads, dim, page, n = 16, 64, 32, before + run
+    each = -(-n // page)
+    cache = make(qv, dev, seqs * each, heads, page, dim, kind, 6)
+    table = torch.arange(seqs * each, dtype=torch.int32, device=dev).view(seqs, each)
+    lens = torch.full((seqs,), n, dtype=torch.int32, device=dev)
+    starts = torch.arange(seqs + 1, dtype=torch.int32, device=dev) * run
+    Q = torch.randn((seqs * run, heads, dim), generator=gen(1)).to(torch.bfloat16).to(dev)
+    work = torch.empty(qv.qv_run_attention_workspace_size(seqs * run, seqs, run, heads, heads, dim, each * page),
+                       dtype=torch.uint8, device=dev)
+
+    def timed():
+        O = torch.empty_like(Q)
+        call = lambda: qv.qv_run_attention(Q, starts, run, cache, table, lens, O, work, window=window, causal=causal)
+        call()
+        return O, fastest(call)
+
+    clean, clean_ms = timed()
+    step = 1 if kind == "int8" else 16  # tokens of a scale
+    for scales in (cache.k_scale, cache.v_scale):
+        per = scales.view(seqs, each, heads, page // step).transpose(2, 3).reshape(seqs, -1, heads)  # a copy, by place
+        per[:, -(-n // step):] = float("nan")
+        if window:  # the first row sees places n - run - window + 1 onwards
+            per[:, :(n - run - window + 1) // step] = float("nan")
+        scales.copy_(per.view(seqs, each, page // step, heads).transpose(2, 3).reshape(scales.shape))
+    got, ms = timed()
+    assert torch.equal(got, clean) and bool(torch.isfinite(got.float()).all())
+    print(f"{kind} {seqs} x {run}: {clean_ms * 1e3:.1f} us, with scales of NaN {ms * 1e3:.1f}")
+    assert ms <= 1.35 * clean_ms, f"{ms * 1e3:.1f} us, {clean_ms * 1e3:.1f} with finite scales"
