@@ -74,6 +74,7 @@ class StreamBlock:
             self.table = torch.arange(sequences * each, dtype=torch.int32, device=device).view(sequences, each)
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
         self.held = [0] * sequences  # the host's copy of lens
+        self.axes = axes
         self.position = torch.zeros((sequences, axes), dtype=torch.int32, device=device)
         w = self.dim // axes
         angle = torch.arange(positions, device=device)[:, None] * base ** (-torch.arange(0, w, 2, device=device) / w)
@@ -120,6 +121,17 @@ class StreamBlock:
         if need > self.left:
             raise ValueError(f"StreamBlock: {need} pages needed, {self.left} of {self.cache.pages} are free")
         return need
+
+    def _check_positions(self, position, rows: int) -> None:
+        """ValueError unless the append takes the positions of ``rows`` tokens: what it refuses comes before they have places."""
+        import torch
+
+        if position is None and self.axes == 1:
+            return  # the places themselves
+        if (not torch.is_tensor(position) or position.dtype != torch.int32 or tuple(position.shape) != (rows, self.axes)
+                or not position.is_contiguous() or position.device != self.lens.device):
+            what = f"{position.dtype} {list(position.shape)} on {position.device}" if torch.is_tensor(position) else type(position).__name__
+            raise ValueError(f"StreamBlock: position is {what}, expected dense int32 [{rows}, {self.axes}] on {self.lens.device}")
 
     def _count(self, runs, need: int) -> None:
         self.held = [n + m for n, m in zip(self.held, runs)]
@@ -182,6 +194,7 @@ class StreamBlock:
         import torch
 
         b = {name: t[:T] if name in self.linears else t for name, t in self.frame.items()}
+        self._check_positions(position, T)
         self._need_room(runs)
         q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=False))
         index = self.lens[sequence] + torch.arange(T, dtype=torch.int32, device=x.device)
@@ -206,6 +219,7 @@ class StreamBlock:
 
         qv, T = self.qv, x.shape[0]
         b = {name: t[:T] if name in self.linears or name in ("q", "o") else t for name, t in self.frame.items()}
+        self._check_positions(position, T)
         need = self._need_room(runs)
         q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=False))
         if self.pooled:
@@ -239,6 +253,7 @@ class StreamBlock:
         qv, b = self.qv, self.one
         captured = torch.cuda.is_current_stream_capturing()  # runs later, see reserve()
         runs = [1] * self.B
+        self._check_positions(self.position, self.B)
         need = 0 if captured else self._need_room(runs)
         q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=True))
         if self.pooled:
