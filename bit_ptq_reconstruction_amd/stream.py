@@ -42,6 +42,9 @@ class StreamBlock:
         self.dim = self.width // heads
         if int8_cache and fp8_cache:
             raise ValueError("StreamBlock: a cache is int8 or FP8")
+        for name, n in (("window", window), ("sinks", sinks)):
+            if not hasattr(n, "__index__") or not 0 <= n < 1 << 63:
+                raise ValueError(f"StreamBlock: {name} {n} is not a number of tokens")
         self.window, self.sinks = window, sinks
         empty = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=device)
         byte = lambda n: empty(n, dtype=torch.uint8)
