@@ -215,7 +215,7 @@ class StreamBlock:
             raise ValueError(f"StreamBlock: runs {runs} of {self.B} sequences for {x.shape[0]} tokens")
         if x.shape[0] > len(self.frame["qkv"]):
             raise ValueError(f"StreamBlock: {x.shape[0]} tokens, the block was made for frames of up to {len(self.frame['qkv'])}")
-        return self._take(x, runs, position, causal)
+        return self._take(x, runs, position, bool(causal))
 
     def _take(self, x, runs, position, causal):
         import torch
@@ -224,6 +224,10 @@ class StreamBlock:
         b = {name: t[:T] if name in self.linears or name in ("q", "o") else t for name, t in self.frame.items()}
         self._check_positions(position, T)
         need = self._need_room(runs)
+        if causal is not None:  # before the tokens have places: there may be no memory for it
+            room = self.table.shape[1] * self.cache.page_size
+            size = qv.qv_run_attention_workspace_size(T, self.B, max(runs), self.heads, self.heads, self.dim, room)
+            parts = torch.empty(size, dtype=torch.uint8, device=x.device)
         q, k, v = self._heads(self._linear("qkv", self._norm(x), b, few=False))
         if self.pooled:
             starts, seq, index = self._places(torch.tensor(runs, dtype=torch.int32, device=x.device), T, b)
@@ -238,9 +242,6 @@ class StreamBlock:
         qv.qv_kv_append(self.cache, self.table, seq, index, k, v, self.cos, self.sin, position, *queries)
         if causal is None:
             return None
-        room = self.table.shape[1] * self.cache.page_size
-        size = qv.qv_run_attention_workspace_size(T, self.B, max(runs), self.heads, self.heads, self.dim, room)
-        parts = torch.empty(size, dtype=torch.uint8, device=x.device)
         qv.qv_run_attention(b["q"], starts, max(runs), self.cache, self.table, self.lens, b["o"], parts, window=self.window,
                             sinks=self.sinks, causal=causal)
         y = x + self._linear("proj", b["o"].view(T, self.width), b, few=False)

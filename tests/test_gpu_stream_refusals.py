@@ -67,3 +67,34 @@ def test_places_as_positions(qv, dev, weights, pages):
     block.take_frame(frame, 0, None)
     other.take_frame(frame, 0, at)
     assert state(block) == state(other)
+
+
+class Short:
+    """The package, with an attention whose workspace no GPU holds."""
+
+    def __init__(self, qv):
+        self.qv = qv
+
+    def __getattr__(self, name):
+        return getattr(self.qv, name)
+
+    def qv_run_attention_workspace_size(self, *sizes):
+        return 1 << 50
+
+
+@pytest.mark.parametrize("pages", [None, 8])
+def test_no_memory(qv, dev, weights, pages):
+    """A workspace that does not fit, or an argument that has no truth value, stops a call before its tokens have places."""
+    g = gen(6)
+    block = make(qv, dev, weights, capacity=64, frame_tokens=40, pages=pages)
+    x, at = rows(40, g, dev), places(40, g, dev)
+    before = state(block)
+    block.qv = Short(qv)
+    with pytest.raises(RuntimeError):
+        block.take_runs(x, [25, 15], at)
+    assert state(block) == before
+    block.qv = qv
+    with pytest.raises(RuntimeError):
+        block.take_runs(x, [25, 15], at, causal=torch.zeros(2))
+    assert state(block) == before
+    assert bool(torch.isfinite(block.take_runs(x, [25, 15], at).float()).all()) and block.held == [25, 15]
