@@ -60,6 +60,14 @@ inline RunTiles run_tiles(int64_t T, int64_t B, int64_t q_heads, int64_t heads, 
   return t;
 }
 
+// Tokens that the rows of a tile see, at most: their windows, which begin up to a tile's rows apart, and the first tokens; all of the
+// run behind them where it is not causal.
+inline int64_t tokens_of_tile(int64_t capacity, int64_t max_run, int64_t window, int64_t sinks, bool causal) {
+  if (window == 0 || window >= capacity) return capacity;
+  const int64_t seen = window + (causal ? kRowsPerTile : max_run) + (sinks < capacity ? sinks : capacity);
+  return seen < capacity ? seen : capacity;
+}
+
 // Whether a call goes that way.  us, few-row kernel and tiles: 16 runs of 5 tokens of 4 query heads over 8192 in bf16 38 and 38, 32 runs
 // of 8 over 4096 73 and 62, one of 48 tokens over 30000 22 and 41; over 8-bit caches, which the tiles convert ahead of their
 // products, 29 to 32 and 53 to 55, 51 to 57 and 80 to 84, 21 to 23 and 51 to 53, one of 16 x 4 rows over 30000 41 to 46 and 55 to 59.

@@ -690,9 +690,8 @@ hipError_t launch_run_tiles(const RunArgs& in, hipStream_t st) {
   t.a.sinks = in.sinks > 0x7fffffff ? 0x7fffffff : (int32_t)in.sinks;
   t.a.causal = in.causal;
   RunTiles tiles = run_tiles(in.T, in.base.B, in.base.q_heads, in.base.cache.heads, t.a.capacity);  // as the workspace was sized
-  const int64_t window = in.base.window;
-  if (window > 0 && window < t.a.capacity - kRows - t.a.sinks)
-    tiles = run_tiles(in.T, in.base.B, in.base.q_heads, in.base.cache.heads, window + kRows + t.a.sinks, tiles.parts);
+  const int64_t seen = tokens_of_tile(t.a.capacity, in.max_run, in.base.window, in.sinks, in.causal);
+  if (seen < t.a.capacity) tiles = run_tiles(in.T, in.base.B, in.base.q_heads, in.base.cache.heads, seen, tiles.parts);
   t.items = tiles.items;
   t.parts = (uint32_t)tiles.parts;
   t.least = (uint32_t)kLeastSteps;
