@@ -65,7 +65,8 @@ def qv_run_attention(Q, starts, max_run: int, cache, page_table, lens, O, worksp
     """O [T, q_heads, D]: attention of each sequence's new tokens, its last ones, over its lens[b] tokens in ``cache``.
 
     Rows starts[b] to starts[b + 1] - 1 of Q [T, q_heads, D] (fp32/bf16) are those of sequence b (starts [B + 1] int32; None:
-    row b is sequence b's one token), up to ``max_run`` of them.  A token sees those up to itself (``causal``) or all of its
+    row b is sequence b's one token), up to ``max_run`` of them (a longer run is its first ``max_run`` rows, taken for the
+    sequence's last tokens).  A token sees those up to itself (``causal``) or all of its
     sequence, and of these the last ``window`` up to itself (0: all) and the first ``sinks``; scale defaults to D ** -0.5.
     ``workspace`` holds at least ``qv_run_attention_workspace_size(T, B, max_run, q_heads, heads, D, page_table.shape[1] *
     page_size)`` bytes."""

@@ -60,15 +60,16 @@ size_t qv_run_attention_workspace_size(int64_t T, int64_t B, int64_t max_run, in
 /*
  * qv_run_attention -- attention of each sequence's new tokens over the paged cache, which holds them already:
  *   O[s][i] = sum_t softmax_t(scale Q[s][i] . k[t][i / (q_heads / heads)]) v[t][i / (q_heads / heads)]
- * Row s of sequence b is its token at place p = lens[b] - n_b + s - starts[b], and sees the tokens t of b with
+ * Row s of sequence b, which has n_b of them, is its token at place p = lens[b] - n_b + s - starts[b], and sees the tokens t of b with
  *   t <= p (causal) or t < lens[b] (causal = 0),  and  t < sinks or t > p - window (window = 0: all of them).
  *   Q           [T][q_heads][head_dim] fp32 or bf16;  q_heads a multiple of the cache's heads.
  *   starts      [B + 1] int32, not falling: rows starts[b] .. starts[b + 1] - 1 are sequence b's n_b, its last ones (cut to
- *               [0, T]); or NULL: row b is sequence b's one token (then T = B and max_run = 1).
+ *               [0, T] and to max_run rows); or NULL: row b is sequence b's one token (then T = B and max_run = 1).
  *   page_table, lens   as for qv_paged_attention, max_pages * page_size below 2^31 - 64.  Tokens on a page outside [0, num_pages)
  *               do not take part.
- *   max_run     the longest run, up to T.  Rows behind the first max_run of a run are not written, nor are rows that no
- *               sequence has.
+ *   max_run     the longest run, up to T (of a captured call, the longest that its replays will have).  A longer run is its
+ *               first max_run rows: n_b is max_run, so that these are taken for the last max_run tokens of the sequence.  Rows
+ *               behind them are not written, nor are rows that no sequence has.
  *   scale       finite;  window >= 0, sinks >= 0.
  *   O           [T][q_heads][head_dim] of Q's type.  A row that sees no token gives zeros; a query of NaN, or a NaN among the
  *               tokens that a row sees, gives NaN; what a row does not see does not count, whatever it holds.

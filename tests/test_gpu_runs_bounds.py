@@ -83,3 +83,26 @@ def test_scales_that_no_row_needs(qv, dev, kind, seqs, before, run, window, caus
     assert torch.equal(got, clean) and bool(torch.isfinite(got.float()).all())
     print(f"{kind} {seqs} x {run}: {clean_ms * 1e3:.1f} us, with scales of NaN {ms * 1e3:.1f}")
     assert ms <= 1.35 * clean_ms, f"{ms * 1e3:.1f} us, {clean_ms * 1e3:.1f} with finite scales"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("run,max_run,window,causal", [(7, 4, 0, True), (20, 9, 11, True), (150, 130, 0, True), (150, 90, 40, False)])
+def test_run_longer_than_said(qv, dev, kind, run, max_run, window, causal):
+    """A run of more than max_run rows is its first max_run, as if there were no others: their places are those of a run of that many.
+    The rows behind them stay."""
+    g = gen(run)
+    lens, starts = [run + 60, run], [0, run, 2 * run]
+    table, pages = shuffled_table(lens, 16, g)
+    cache = make(qv, dev, pages, 2, 16, 64, kind, 7)
+    Q = torch.randn((2 * run, 4, 64), generator=g).to(torch.bfloat16)
+    O = attend(qv, dev, Q.to(dev), starts, max_run, cache, table, lens, window, 3 if window else 0, causal)
+    for b in range(2):
+        part = Q[b * run:b * run + max_run].to(dev).contiguous()
+        one = attend(qv, dev, part, [0, max_run], max_run, cache, table[b:b + 1], lens[b:b + 1], window, 3 if window else 0, causal)
+        # the two calls may cut the tokens differently: each is held to its bound
+        got = O[b * run:b * run + max_run].double().cpu()
+        o, mag, _ = runs64(Q[b * run:b * run + max_run], [0, max_run], cache, table[b:b + 1], lens[b:b + 1], window,
+                           3 if window else 0, causal, 0.125)
+        for x in (got, one.double().cpu()):
+            assert ((x - o).abs() / ((1e-5 + LOST) * mag + 1.01 * BF * o.abs() + 1e-38)).max().item() <= 1.0
+        assert bool(torch.isnan(O[b * run + max_run:(b + 1) * run].float()).all())
