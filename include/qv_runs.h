@@ -42,8 +42,10 @@ typedef enum {
  *               among all slots of the cache, page * page_size + place % page_size.  Rows of a sequence that is refused, and
  *               rows from starts[B] on, are -1 (which qv_kv_append does not store).
  *   status      [B] int32 out: qv_run_status.  A sequence is refused as a whole: it takes no pages and keeps its length, but
- *               its rows stay its own (what attention makes of them means nothing).  Sequences are served in order: one that lacks pages has asked for them all the same, so
- *               that no later one that needs a page gets any.  A sequence without new tokens is never refused for pages or rows.
+ *               its rows stay its own (what attention makes of them means nothing).  One without room or rows asks for no
+ *               pages, whatever is free.  Sequences are served in order: one that lacks pages has asked for them all the same,
+ *               so that no later one that needs a page gets any.  A sequence without new tokens is never refused for pages or
+ *               rows.
  * Outputs other than those two, and the table, do not overlap the inputs or each other.
  * The page of a place before lens[b] is read from the table.  T = 0 is accepted with null outputs of [T].  T <= 2^31 - 1.
  */

@@ -1,4 +1,5 @@
-"""Attention of runs of tokens: what the probabilities' pieces leave of them, and what tokens that no row sees cost.
+"""Runs of tokens: what the probabilities' pieces leave of them, what tokens that no row sees cost, runs longer than said, and which
+sequences ask for pages.
 
 The probabilities of a bf16 query are two bf16 pieces, each to the nearest: one in [1, 2) leaves at most 2^-8 to the second,
 whose last place is then 2^-16, so that 2^-17 of it is lost at most.  With the rest of test_gpu_runs' bound an element is held to
@@ -106,3 +107,23 @@ def test_run_longer_than_said(qv, dev, kind, run, max_run, window, causal):
         for x in (got, one.double().cpu()):
             assert ((x - o).abs() / ((1e-5 + LOST) * mag + 1.01 * BF * o.abs() + 1e-38)).max().item() <= 1.0
         assert bool(torch.isnan(O[b * run + max_run:(b + 1) * run].float()).all())
+
+
+@pytest.mark.parametrize("T,last", [(200, 3), (3000, 2)])  # the last run: its rows pass T, or there are no pages
+def test_who_asks_for_pages(qv, dev, T, last):
+    """A sequence without room asks for no pages, so that the next one gets some; one that lacks pages has asked for them."""
+    runs = [20, 60, 10, 30, 40, 16, 3, 50, 0]
+    lens = [0, 5, 20, 16, 0, 16, 33, 0, 64]  # in tables of 4 pages of 16
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+    empty = lambda n, dtype=torch.int32: torch.full((n,), -7, dtype=dtype, device=dev)
+    B = len(runs)
+    table = torch.full((B, 4), 99, dtype=torch.int32, device=dev)
+    starts, after, left, seq, index, slots, status = (empty(B + 1), empty(B), empty(1), empty(T), empty(T),
+                                                      empty(T, torch.int64), empty(B))
+    qv.qv_page_tables(i32(runs), i32(lens), i32([5, 9, 3, 8, 1, 7]), i32([5]), 16, table, starts, after, left, seq, index,
+                      slots, status)
+    assert status.tolist() == [0, 1, 0, 0, 2, 2, 0, last, 0] and left.tolist() == [1]
+    assert after.tolist() == [20, 5, 30, 46, 0, 16, 36, 0, 64]
+    expect = [[99] * 4 for _ in runs]
+    expect[0][:2], expect[3][1:3] = [1, 8], [3, 9]  # from the end of the five that count
+    assert table.tolist() == expect
