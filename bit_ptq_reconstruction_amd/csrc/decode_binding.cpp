@@ -462,6 +462,7 @@ PyObject* run_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t window = whole(a[9]), sinks = whole(a[10]);
     if (window < 0) c.bad("window " + std::to_string(window) + " must not be negative");
     if (sinks < 0) c.bad("sinks " + std::to_string(sinks) + " must not be negative");
+    if (!std::isfinite((float)scale)) c.bad("scale " + std::to_string(scale) + " must be finite");
     const int causal = PyObject_IsTrue(a[11]);
     if (causal < 0) throw Raised{};
     void* w = c.workspace(

@@ -3,6 +3,8 @@
 // launches nothing and touches no device state.
 #include "qv_runs.h"
 
+#include <cmath>
+
 #include "qv_decode_checks.h"
 #include "qv_runs_internal.h"
 
@@ -73,7 +75,7 @@ qv_status qv_run_attention(const qv_heads* Q, qv_dtype q_dtype, int64_t T, int64
     st = check_table(page_table, B, max_pages, ld_table, cache);
     if (st != QV_OK) return st;
     if (T < 0 || q_heads <= 0 || q_heads > 65536 || q_heads % cache->heads != 0 || window < 0 || sinks < 0 || max_run < 0 ||
-        max_run > T)
+        max_run > T || !std::isfinite(scale))
       return QV_ERR_SHAPE;
     if (!starts && (T != B || max_run > 1)) return QV_ERR_SHAPE;
     const int64_t capacity = max_pages * cache->page_size;

@@ -72,7 +72,7 @@ size_t qv_run_attention_workspace_size(int64_t T, int64_t B, int64_t max_run, in
  *   max_run     the longest run, up to T (of a captured call, the longest that its replays will have).  A longer run is its
  *               first max_run rows: n_b is max_run, so that these are taken for the last max_run tokens of the sequence.  Rows
  *               behind them are not written, nor are rows that no sequence has.
- *   scale       finite;  window >= 0, sinks >= 0.
+ *   scale       finite;  window >= 0, sinks >= 0 (else QV_ERR_SHAPE).
  *   O           [T][q_heads][head_dim] of Q's type.  A row that sees no token gives zeros; a query of NaN, or a NaN among the
  *               tokens that a row sees, gives NaN; what a row does not see does not count, whatever it holds.
  *               Scores, softmax and sums are fp32.  For the product with the values, bf16 queries in runs with more than
