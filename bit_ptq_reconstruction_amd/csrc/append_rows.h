@@ -60,8 +60,6 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
   }
 }
 
-// R: heads of a thread, all of one token and `groups` apart, so that neighbouring threads have neighbouring heads; they
-// share the token's place and its cosines and sines.
 inline Rows rows_of(const qv_heads& h) { return {h.data, h.token_stride, h.head_stride}; }
 
 }  // namespace

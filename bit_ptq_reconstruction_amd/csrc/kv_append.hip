@@ -50,6 +50,8 @@ __device__ __forceinline__ void store8(int8_t* p, const float (&v)[8], float sca
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
+// R: heads of a thread, all of one token and `groups` apart, so that neighbouring threads have neighbouring heads; they
+// share the token's place and its cosines and sines.
 template <int D, typename X, bool INT8, int R>
 __global__ __launch_bounds__(kThreads) void append_kernel(Args a) {
   constexpr int kParts = D / 16;

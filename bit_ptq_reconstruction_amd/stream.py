@@ -19,7 +19,8 @@ class StreamBlock:
 
     ``cache`` holds bf16, int8 with a scale per token (``int8_cache``) or float8_e4m3fn with a scale per page
     (``fp8_cache``).  A token sees the last ``window`` tokens up to itself (0: all) and the first ``sinks``.  With ``pages`` the
-    sequences share that many pages and take them as they grow (end() gives a sequence's back); else each has its own.
+    sequences share that many pages and take them as they grow (end() gives a sequence's back; a window gives none back, so that
+    a sequence ends at ``capacity`` with one as well); else each has its own.
 
     The block has no biases, no weights in its norms and no smoothing.
 
@@ -28,8 +29,9 @@ class StreamBlock:
     sums are torch's and allocate theirs (under capture from the graph's pool), and so do take_frame()
     and take_runs(), which reads its runs on the host and is not for capture.
 
-    ``positions`` places along each of ``axes`` axes have an angle; the output of a token at another one, and of those that
-    come after it in its sequence, is NaN.  A frame, or the runs of one call, has up to ``frame_tokens`` tokens."""
+    ``positions`` places along each of ``axes`` axes have an angle; the output of a token at another one is NaN, and so is that of
+    the tokens that attend to it: those that come after it in its sequence (or with it, where a run is not causal) as long as
+    it is among the last ``window`` or first ``sinks`` tokens.  A frame, or the runs of one call, has up to ``frame_tokens`` tokens."""
 
     def __init__(self, qv, weights, sequences: int, capacity: int, device, heads: int = 16, axes: int = 1,
                  positions: int = 4096, base: float = 10000.0, int8_cache: bool = False, page_size: int = 64,
