@@ -43,9 +43,9 @@ struct RunTiles {
 // with two or more, so a call takes about (blocks of the CU that has most) x (steps of a block and its start), half as much again where
 // that is one block; each part costs the join as much as a step.  `seen`: tokens that a tile's rows see, at most; `room`: parts
 // that the workspace holds.
-// us with 1, 2, 3, 4, 5, 6, 8 and 12 parts, and as chosen: a frame over eight 170 123 112 99 111 112 109 120, 101; a chunk of two prompts
-// over 4001 in FP8 139 102 107 95 94 108 110 123, 98; 256 tokens (8 heads of 128, 32 queries) over 100000 1918 974 660 506 503 467 416
-// 491, 443; eight chunks of 128 over 4000 89 66 50 57 54 54 59 64, 57; one prompt of 2048 60 76 85 96 56 58 60 58, 59.
+// us with 1, 2, 3, 4, 5, 6, 8 and 12 parts, and as chosen: a frame over eight 205 137 143 120 134 129 126 134, 120; a chunk of two prompts
+// over 4001 in FP8 164 114 114 101 98 111 108 122, 101; 8 heads of 128 with 32 queries, 256 tokens over 100000 2590 1310 882 685 740 660
+// 581 637, 616, eight chunks of 128 over 4000 157 118 125 126 131 134 154 178, 125, one prompt of 2048 75 85 97 109 105 113 127 126, 75.
 inline RunTiles run_tiles(int64_t T, int64_t B, int64_t q_heads, int64_t heads, int64_t seen, int64_t room = kMostParts) {
   RunTiles t;
   t.items = T * (q_heads / heads) / kRowsPerTile + B;
@@ -68,9 +68,11 @@ inline int64_t tokens_of_tile(int64_t capacity, int64_t max_run, int64_t window,
   return seen < capacity ? seen : capacity;
 }
 
-// Whether a call goes that way.  us, few-row kernel and tiles: 16 runs of 5 tokens of 4 query heads over 8192 in bf16 38 and 38, 32 runs
-// of 8 over 4096 73 and 62, one of 48 tokens over 30000 22 and 41; over 8-bit caches, which the tiles convert ahead of their
-// products, 29 to 32 and 53 to 55, 51 to 57 and 80 to 84, 21 to 23 and 51 to 53, one of 16 x 4 rows over 30000 41 to 46 and 55 to 59.
+// Whether a call goes that way.  us, few-row kernel and tiles, over bf16: 16 runs of 5 tokens of 4 query heads over up to 8192 41 and 48,
+// 32 of 8 over 4096 88 and 79, 64 of 10 over 2000 129 and 77, four of 40 (16 heads of 64) over 4000 30 and 28; over 8-bit caches, which
+// the tiles convert ahead of their products, 32 to 34 and 59 to 62, 69 to 74 and 93 to 97, 98 to 109 and 96 to 102, 27 to 28 and 34 to 35.
+// Heads, sequences and past are not in the rule: one run of 48, 64 or 128 tokens over 30000 with two heads gives the tiles few blocks and
+// takes 23, 25 and 36 against 49 to 50 over bf16, 21 to 23, 24 to 26 and 31 to 35 against 58 to 62 over 8-bit caches.
 inline bool long_runs(int64_t max_run, int64_t q_heads, int64_t heads, bool bytes) {
   return max_run > 1 && max_run * (q_heads / heads) > (bytes ? QV_RUN_FEW_ROWS_8BIT : QV_RUN_FEW_ROWS);
 }

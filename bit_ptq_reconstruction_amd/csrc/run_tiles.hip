@@ -15,16 +15,17 @@
 // bf16 queries: a probability is two bf16 pieces for the second product, each to the nearest, which leave 2^-17 of it at most and of
 // either sign, of the order of its score's fp32 rounding; their sum is of the whole ones.  One piece, with two thirds of
 // the matrix instructions, leaves 2^-8 and a result that is 2.1 to 2.3e-3 off in the 2-norm where its own rounding makes 1.6 to
-// 1.7e-3 (us with one piece and with two: frame over eight 89 and 116, chunk in FP8 91 and 102, prompts of up to 8192 982 and 1369).
+// 1.7e-3 (us with one piece and with two: frame over eight 89 and 116 to 119, chunk in FP8 91 and 102, prompts of up to 8192 982 and 1350 to 1390).
 // fp32 queries and their probabilities are three bf16 pieces that sum to them.
 // The maximum that scales a row's probabilities is raised only when one passes 2^8 of it: sums are fp32, and the rest follows.
 //
-// Bound by the matrix cores and the vector ALU (32 exponentials, 32 multiply-adds and 32 sums of a lane to 32 matrix instructions of
-// 128 channels) together: four prompts of up to 8192 tokens (8 heads of 128, 32 queries, causal) take 1.37 ms, 0.73
-// PFLOP/s, where a library product of 8192^3 reaches 1.22: the second product's two pieces make it half as many matrix instructions
-// again (1.10 PFLOP/s).  A frame of 1374 tokens over eight (16 heads of 64) takes 116 us, 535 TFLOP/s: with 64 channels the vector ALU
-// has twice as much to do for a matrix instruction.  A chunk of up to 611 tokens over 4001 of the FP8 cache 99 us (conversions,
-// join), fp32 prompts of up to 1833 tokens with a window of 1000 in 42 us (one wave a SIMD, 1100 waves of a dozen steps).
+// Bound by the matrix cores and the vector ALU (32 exponentials, 32 multiply-adds, 32 sums and the pieces of 32 probabilities of a lane
+// to 48 matrix instructions of 128 channels) together: four prompts of up to 8192 tokens (8 heads of 128, 32 queries, causal) take 1.35
+// to 1.39 ms, 0.72 to 0.74 PFLOP/s with each product counted once and 1.08 to 1.12 as they are made, where a library product of 8192^3
+// reaches 1.22; the matrix cores are busy for 54 % of the time, the vector ALU for 51 %.  A frame of 1374 tokens over eight (16 heads of
+// 64) takes 116 to 119 us with its join, 520 to 535 TFLOP/s: with 64 channels the vector ALU has twice as much to do for a matrix
+// instruction (58 and 36 % busy).  A chunk of up to 611 tokens over 4001 of the FP8 cache takes 99 to 100 us (conversions, join), fp32
+// prompts of up to 1833 tokens with a window of 1000 43 us (one wave a SIMD, 1100 waves of a dozen steps).
 //
 // Tried with one piece to a probability (us: frame over eight, prompts of 8192): staging bf16 by way of registers and masks in every step 179, 1505; steps whose
 // way depends on masks only through a branch that changes scores 133, 1089; scalar addresses for the loads to LDS 140, 962 where it was
